@@ -340,7 +340,7 @@ def encode8(state8, m, v, dither_m, dither_v):
     for x, top, low, most, codes, scales, add in ((m, 448.0, 2.0**-120, 126, mc, ms, dither_m),
                                                   (v, 1.875, 2.0**-96, 255, vc, vs, dither_v)):
         peak = x.abs().amax(1, keepdim=True)
-        some = peak >= 2.0**-110  # a block below is held as zeros
+        some = ~(peak < 2.0**-110)  # a block below is held as zeros
         scale = torch.where(some, peak * (1 / top), 0.0)
         inverse = torch.where(some, torch.full_like(peak, top) / peak, 0.0)
         # scaled so that the code is the top bits of the fp32 pattern, subnormals included
