@@ -385,6 +385,184 @@ int zero_adamw_step_dev(const void* grad_dev, zero_dtype gdt, float* master_dev,
 int zero_adamw_step_tiled_dev(const void* grad_dev, zero_dtype gdt, float* state_dev, uint16_t* param_dev,
                               zero_dtype pdt, int64_t n, const zero_step_state* step_state_dev, void* stream);
 
+/* ------------------------------------------------------------------ lists of tensors
+ *
+ * The norm and the update over many tensors at once, where they lie: the
+ * gradients are read from their own buffers and the parameters written to
+ * theirs, with no flat copy in between (a list's step moves 30 B/param, the
+ * flattened one 32).  A list can hold whole tensors (data parallelism without
+ * sharding) or a rank's pieces of them (zero_shard_layout's segments).  The
+ * tensors of a list may differ in size, format, state layout and group.
+ *
+ *   zero_list_plan            checks a list and builds its device table
+ *   zero_list_grad_sqnorm     fp64 sum of squares and inf/NaN flag
+ *   zero_list_decision_dev    the decision, with the scalars of every group
+ *   zero_list_adamw_step      AdamW with fp32 state
+ *   zero_list_adamw8_step     AdamW with the moments held in 8 bits
+ *   zero_list_state8_pack     fp32 moments -> 8 bits; _unpack: back
+ */
+
+/* Third format, of gradients and parameters in lists only. */
+enum { ZERO_FP32 = 2 };
+
+/* How a tensor's optimizer state is laid out. */
+enum {
+  ZERO_STATE_NONE = 0,   /* no state (norm only): state, m, v NULL */
+  ZERO_STATE_ARRAYS = 1, /* state = fp32 master[numel], m[numel], v[numel]; 4-byte aligned */
+  ZERO_STATE_TILED = 2,  /* state = zero_state_tiled_numel(numel) floats, 16-byte aligned; m, v NULL */
+  ZERO_STATE_8BIT = 3    /* state = zero_state8_bytes(numel) bytes, 16-byte aligned; m, v NULL */
+};
+
+/* 8-bit state.  Moments are held in blocks of ZERO_STATE8_BLOCK elements with
+ * one fp32 scale per block and moment:
+ *   m = value4(code) * scale:  sign, 4 exponent and 3 fraction bits with
+ *       subnormals (the OCP e4m3 format: bias 7, largest 448);
+ *   v = value5(code) * scale:  5 exponent and 3 fraction bits, no sign, with
+ *       subnormals (bias 31, largest 1.875): 32 octaves, as the second moment
+ *       is a square.
+ * The fp32 master stays.  A tile of ZERO_STATE8_TILE elements holds
+ *   float master[4096]; uint8 m[4096]; uint8 v[4096]; float m_scale[16];
+ *   float v_scale[16];                                  (24,704 bytes)
+ * and a tensor's last tile is padded; padding is never written.
+ *
+ * Encoding a block (updates and pack): peak = the largest |m| (v) of the
+ * block; a block whose peak is below 2^-110 is held as zeros, scale 0.
+ * scale = peak / 448 (peak / 1.875, by a multiplication with the fp32
+ * reciprocal of the constant), and x·(448/peak) (1.875/peak) is rounded to a
+ * code.  A v that is not zero never takes code 0.  A NaN or infinity in a
+ * block makes its scale NaN or infinite: the whole block then reads as not
+ * finite (a step whose norm flagged it is to be skipped, as ever).
+ *   Updates round stochastically: position p between two codes k and k+1 goes
+ * to k+1 with probability p - k, so the expected value is the value.  With
+ * rounding to nearest the second moment would stand still: a step changes it
+ * by a factor of 1 - beta2 or less, far below half the distance of two codes
+ * (3 to 6%).  The dither is a counter hash, the same for the same arguments:
+ *   base = mix(seed + G·t), key(b) = mix(base + G·(b + 1)), all mod 2^64,
+ *   mix = SplitMix64's output function, G = 0x9E3779B97F4A7C15, t the Adam step,
+ *   b = the block's number in the list (every tensor counts whole tiles: 16
+ *   blocks each), and r(j) = (key(b) + j·0x9E3779B9) mod 2^32 for element j of
+ *   the block: m takes the upper 20 bits of r, v the lower 20.
+ *   Pack rounds to nearest. */
+#define ZERO_STATE8_BLOCK 256
+#define ZERO_STATE8_TILE 4096
+/* Bytes of the 8-bit state of n elements (0 for n <= 0 or n > ZERO_MAX_NUMEL). */
+int64_t zero_state8_bytes(int64_t n);
+
+/* One tensor (or piece) of a list. */
+typedef struct zero_list_tensor {
+  const void* grad;  /* numel gradients in format gdt; NULL: no gradient in this step, the tensor is left as it is */
+  void* param;       /* numel parameters in format pdt, written by the updates (never read); NULL: none */
+  void* state;       /* see the layouts above */
+  float* m;          /* ZERO_STATE_ARRAYS only */
+  float* v;
+  int64_t numel;     /* in [0, 2^40] */
+  zero_dtype gdt;    /* ZERO_BF16, ZERO_FP16 or ZERO_FP32 */
+  zero_dtype pdt;
+  int32_t layout;    /* ZERO_STATE_* */
+  int32_t group;     /* which hyper-parameters: in [0, n_groups) */
+} zero_list_tensor;
+
+#define ZERO_LIST_MAX_GROUPS 64
+
+/* A planned list, filled by zero_list_plan.  Host memory, the caller's.  Only
+ * table_dev is for the caller to set: the device address of its copy of the
+ * table (16-byte aligned), which must stay as planned while calls use it. */
+typedef struct zero_list {
+  const void* table_dev;
+  int64_t table_bytes;   /* size of the table */
+  int64_t grads_bytes;   /* its leading part, all that zero_list_repoint changes */
+  int64_t numel;         /* elements of all tensors */
+  int64_t norm_blocks;   /* workgroups of the norm */
+  int64_t update_blocks; /* workgroups of the update (0 without state) */
+  int64_t norm_offset;   /* where the table's parts begin, in bytes */
+  int64_t update_offset;
+  uint64_t shape;        /* fingerprint of the tensors' sizes */
+  uint64_t check;        /* over the fields above but table_dev: a list that was not planned is refused */
+  int32_t n_tensors;
+  int32_t n_groups;
+  int32_t state;         /* 0: none, 32: fp32 (arrays, tiled or both), 8: 8-bit */
+  int32_t flags;         /* ZERO_LIST_* */
+} zero_list;
+enum {
+  ZERO_LIST_HAS_PARAMS = 1, /* every tensor has a param */
+  ZERO_LIST_WHOLE_STATE = 2 /* every tensor has master, m and v */
+};
+
+/* Host only.  Bytes of the table of these tensors (only the sizes and layouts
+ * are looked at); 0 if they are not valid. */
+int64_t zero_list_table_bytes(const zero_list_tensor* tensors, int32_t n_tensors);
+
+/* Host only.  Checks the list, fills *out (table_dev NULL) and writes the
+ * table to table_host (table_bytes >= zero_list_table_bytes, else
+ * ZERO_ERR_CAPACITY), which the caller copies to the device.
+ * Refused (ZERO_ERR_INVALID): unknown formats or layouts, fp32 and 8-bit
+ * state in one list, buffers not aligned to their element size (tiled and
+ * 8-bit state: 16 bytes), sizes or groups out of range, a state buffer
+ * missing, and any overlap of a buffer that an update writes (state, params)
+ * with another buffer of the list; gradients may share memory.
+ *   With ZERO_STATE_ARRAYS any of state, m and v may be NULL: such a list can
+ * only be the source or target of a conversion (a NULL target part is not
+ * written, a NULL source part reads as zeros).  Tensors of no elements are
+ * valid and are passed over. */
+int zero_list_plan(const zero_list_tensor* tensors, int32_t n_tensors, int32_t n_groups, void* table_host,
+                   int64_t table_bytes, zero_list* out);
+
+/* Host only.  The same list with other addresses (the next step's gradients,
+ * some of them perhaps NULL): checks it and rewrites the first
+ * list->grads_bytes bytes of table_host, which the caller copies over the
+ * device table's.  Sizes, layouts and groups must be the planned ones. */
+int zero_list_repoint(const zero_list_tensor* tensors, int32_t n_tensors, void* table_host, int64_t table_bytes,
+                      const zero_list* list);
+
+/* Device.  What zero_grad_sqnorm does, over the gradients of every tensor that
+ * has one.  Deterministic for a given list.  ws_dev: 16-byte aligned, at least
+ * zero_list_grad_sqnorm_workspace_bytes(list) bytes; calls that may overlap in
+ * time need a workspace each. */
+size_t zero_list_grad_sqnorm_workspace_bytes(const zero_list* list);
+int zero_list_grad_sqnorm(const zero_list* list, void* ws_dev, size_t ws_bytes, double* sqnorm_dev,
+                          int32_t* nonfinite_dev, void* stream);
+
+/* Device.  zero_adamw_step's operations, bit for bit, on every tensor that has
+ * a gradient; hp[list->n_groups] on the host, one for each group (the
+ * parameter is rounded to its format as ever, ZERO_FP32 takes the master).
+ * The list must have params and whole fp32 state. */
+int zero_list_adamw_step(const zero_list* list, const zero_adamw_hparams* hp, void* stream);
+
+/* Device.  The same with 8-bit state: the moments are decoded, take
+ * zero_adamw_step's operations (the parameter and the master come from the new
+ * moments before they are rounded) and are encoded again.  eps >= 1e-16 for
+ * every group (a second moment whose block is held as zeros reads as 0).
+ * Every group's hp must have the same step, which with seed sets the dither. */
+int zero_list_adamw8_step(const zero_list* list, const zero_adamw_hparams* hp, uint64_t seed, void* stream);
+
+/* Scalars of one group on the device: those of zero_step_state. */
+typedef struct zero_group_scalars {
+  float scalars[12];
+} zero_group_scalars;
+
+/* Device.  zero_step_decision_dev for n_groups groups: the same decision into
+ * *state_dev (whose own scalars become group 0's), and, unless the step is
+ * skipped, the scalars of every group into groups_dev[n_groups] (16-byte
+ * aligned).  hp[n_groups] on the host: lr, beta1, beta2, eps and weight_decay
+ * are used.  n_groups in [1, ZERO_LIST_MAX_GROUPS]. */
+int zero_list_decision_dev(const double* rank_sqnorms_dev, const int32_t* rank_flags_dev, int32_t n_ranks,
+                           double max_norm, const zero_adamw_hparams* hp, int32_t n_groups,
+                           zero_step_state* state_dev, zero_group_scalars* groups_dev, void* stream);
+
+/* Device.  The updates with the scalars and the Adam step taken from the
+ * device (groups_dev[list->n_groups]); when state_dev->skip is set they return
+ * without touching memory. */
+int zero_list_adamw_step_dev(const zero_list* list, const zero_step_state* state_dev,
+                             const zero_group_scalars* groups_dev, void* stream);
+int zero_list_adamw8_step_dev(const zero_list* list, const zero_step_state* state_dev,
+                              const zero_group_scalars* groups_dev, uint64_t seed, void* stream);
+
+/* Device.  Conversion between a list with fp32 state and a list of the same
+ * sizes with 8-bit state (masters are copied; gradients and parameters are not
+ * touched).  The two lists' states must not overlap. */
+int zero_list_state8_pack(const zero_list* from32, const zero_list* to8, void* stream);
+int zero_list_state8_unpack(const zero_list* from8, const zero_list* to32, void* stream);
+
 /* ------------------------------------------------------------------ measurement aid
  *
  * Not a step of the method: the read-modify-write ceiling of the tiled

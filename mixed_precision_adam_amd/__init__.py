@@ -2,7 +2,7 @@
 
 Argument marshalling only.  Every function has the name of the C entry point
 it wraps (declared in include/zero_shard.h); all device work runs in the HIP
-kernels of ``csrc/zero_shard.hip``.  PyTorch supplies device memory and the
+kernels of ``csrc/zero_shard.hip`` and ``csrc/zero_list.hip``.  PyTorch supplies device memory and the
 stream.  There is no fallback: if the library is missing, importing this
 package raises.
 """
@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libzero_shard.so")
 
 ZERO_BF16 = 0
 ZERO_FP16 = 1
+ZERO_FP32 = 2  # gradients and parameters of lists only
 ZERO_OK, ZERO_ERR_INVALID, ZERO_ERR_CAPACITY, ZERO_ERR_HIP = 0, -1, -2, -3
 
 if not os.path.exists(LIB_PATH):
@@ -107,6 +108,10 @@ _lib.zero_flatten_grads_sqnorm_noalloc.argtypes = [_P, C.c_int32, C.c_int, _P, C
 _lib.zero_calibrate_tiled_rmw.argtypes = [_P, _P, _P, C.c_int64, C.c_uint32, _P]
 
 ZERO_STATE_TILE = 1024  # include/zero_shard.h
+ZERO_STATE8_BLOCK, ZERO_STATE8_TILE = 256, 4096
+ZERO_STATE_NONE, ZERO_STATE_ARRAYS, ZERO_STATE_TILED, ZERO_STATE_8BIT = 0, 1, 2, 3
+ZERO_LIST_MAX_GROUPS = 64
+ZERO_LIST_HAS_PARAMS, ZERO_LIST_WHOLE_STATE = 1, 2
 
 
 class zero_step_state(C.Structure):
@@ -115,6 +120,44 @@ class zero_step_state(C.Structure):
                 ("growth_interval", C.c_int32), ("skip", C.c_int32), ("error", C.c_int32),
                 ("scalars", C.c_float * 12)]
 
+
+
+class zero_list_tensor(C.Structure):
+    _fields_ = [("grad", C.c_void_p), ("param", C.c_void_p), ("state", C.c_void_p), ("m", C.c_void_p),
+                ("v", C.c_void_p), ("numel", C.c_int64), ("gdt", C.c_int32), ("pdt", C.c_int32),
+                ("layout", C.c_int32), ("group", C.c_int32)]
+
+
+class zero_list(C.Structure):
+    _fields_ = [("table_dev", C.c_void_p), ("table_bytes", C.c_int64), ("grads_bytes", C.c_int64),
+                ("numel", C.c_int64), ("norm_blocks", C.c_int64), ("update_blocks", C.c_int64),
+                ("norm_offset", C.c_int64), ("update_offset", C.c_int64), ("shape", C.c_uint64),
+                ("check", C.c_uint64), ("n_tensors", C.c_int32), ("n_groups", C.c_int32), ("state", C.c_int32),
+                ("flags", C.c_int32)]
+
+
+class zero_group_scalars(C.Structure):
+    _fields_ = [("scalars", C.c_float * 12)]
+
+
+_LIST = C.POINTER(zero_list)
+_lib.zero_state8_bytes.argtypes = [C.c_int64]
+_lib.zero_state8_bytes.restype = C.c_int64
+_lib.zero_list_table_bytes.argtypes = [_P, C.c_int32]
+_lib.zero_list_table_bytes.restype = C.c_int64
+_lib.zero_list_plan.argtypes = [_P, C.c_int32, C.c_int32, _P, C.c_int64, _LIST]
+_lib.zero_list_repoint.argtypes = [_P, C.c_int32, _P, C.c_int64, _LIST]
+_lib.zero_list_grad_sqnorm_workspace_bytes.argtypes = [_LIST]
+_lib.zero_list_grad_sqnorm_workspace_bytes.restype = C.c_size_t
+_lib.zero_list_grad_sqnorm.argtypes = [_LIST, _P, C.c_size_t, _P, _P, _P]
+_lib.zero_list_adamw_step.argtypes = [_LIST, _P, _P]
+_lib.zero_list_adamw8_step.argtypes = [_LIST, _P, C.c_uint64, _P]
+_lib.zero_list_decision_dev.argtypes = [_P, _P, C.c_int32, C.c_double, _P, C.c_int32, _P, _P, _P]
+_lib.zero_list_adamw_step_dev.argtypes = [_LIST, _P, _P, _P]
+_lib.zero_list_adamw8_step_dev.argtypes = [_LIST, _P, _P, C.c_uint64, _P]
+_lib.zero_list_state8_pack.argtypes = [_LIST, _LIST, _P]
+_lib.zero_list_state8_unpack.argtypes = [_LIST, _LIST, _P]
+
 # Every symbol include/zero_shard.h declares.
 EXPORTS = ("zero_last_error", "zero_shard_layout", "zero_flatten_plan", "zero_bucket_segments", "zero_flatten_grads",
            "zero_flatten_grads_sqnorm", "zero_flatten_partials_count", "zero_flatten_grads_partials",
@@ -122,7 +165,11 @@ EXPORTS = ("zero_last_error", "zero_shard_layout", "zero_flatten_plan", "zero_bu
            "zero_clip_coef", "zero_loss_scale_update", "zero_cosine_lr", "zero_adamw_step", "zero_state_tiled_numel",
            "zero_adamw_step_tiled", "zero_state_tile", "zero_state_untile", "zero_step_state_init",
            "zero_step_decision_dev", "zero_adamw_step_dev", "zero_adamw_step_tiled_dev",
-           "zero_flatten_grads_sqnorm_noalloc", "zero_calibrate_tiled_rmw")
+           "zero_flatten_grads_sqnorm_noalloc", "zero_calibrate_tiled_rmw", "zero_state8_bytes",
+           "zero_list_table_bytes", "zero_list_plan", "zero_list_repoint", "zero_list_grad_sqnorm_workspace_bytes",
+           "zero_list_grad_sqnorm", "zero_list_adamw_step", "zero_list_adamw8_step", "zero_list_decision_dev",
+           "zero_list_adamw_step_dev", "zero_list_adamw8_step_dev", "zero_list_state8_pack",
+           "zero_list_state8_unpack")
 ZERO_STEP_ERR_LOSS_SCALE = 1  # zero_step_state.error: the decision could not be taken
 ZERO_NOALLOC_SCRATCH_BYTES = 6 << 20  # static scratch of zero_flatten_grads_sqnorm_noalloc, per device
 
@@ -375,6 +422,112 @@ def zero_adamw_step_tiled_dev(grad, dtype: int, state, param, n: int, step_state
     _check(_lib.zero_adamw_step_tiled_dev(_buf(grad, 2 * k), dtype, _buf(state, 4 * zero_state_tiled_numel(k)),
                                           _buf(param, 2 * k), param_dtype, n, _buf(step_state, _STATE),
                                           _stream(stream)))
+
+
+# ---------------------------------------------------------------------- lists of tensors
+
+_ELEM = {ZERO_BF16: 2, ZERO_FP16: 2, ZERO_FP32: 4}
+
+
+def zero_state8_bytes(n: int) -> int:
+    return int(_lib.zero_state8_bytes(n))
+
+
+def zero_list_hparams(groups):
+    """The hyper-parameters of every group of a list (dicts of lr, beta1, beta2, eps, weight_decay and, for updates
+    with host scalars, grad_scale and step), marshalled once: a program keeps the array and changes its fields."""
+    return (zero_adamw_hparams * len(groups))(*[
+        zero_adamw_hparams(g["lr"], g["beta1"], g["beta2"], g["eps"], g["weight_decay"], g.get("grad_scale", 1.0),
+                           g.get("step", 1)) for g in groups])
+
+
+def _list_tensors(tensors):
+    """Dicts with the fields of zero_list_tensor -> a C array, every tensor's size checked against what the call
+    will touch."""
+    out = (zero_list_tensor * max(len(tensors), 1))()
+    for t, rec in zip(tensors, out):
+        n, layout = int(t["numel"]), t.get("layout", ZERO_STATE_NONE)
+        k = max(n, 0)
+        rec.numel, rec.layout, rec.group = n, layout, t.get("group", 0)
+        rec.gdt, rec.pdt = t.get("gdt", ZERO_BF16), t.get("pdt", ZERO_BF16)
+        held = {ZERO_STATE_TILED: 4 * zero_state_tiled_numel(k), ZERO_STATE_8BIT: zero_state8_bytes(k)}.get(layout, 4 * k)
+        rec.grad = _buf(t.get("grad"), k * _ELEM.get(rec.gdt, 4))
+        rec.param = _buf(t.get("param"), k * _ELEM.get(rec.pdt, 4))
+        rec.state, rec.m, rec.v = _buf(t.get("state"), held), _buf(t.get("m"), 4 * k), _buf(t.get("v"), 4 * k)
+    return out
+
+
+def zero_list_table_bytes(tensors) -> int:
+    return int(_lib.zero_list_table_bytes(C.cast(_list_tensors(tensors), _P), len(tensors)))
+
+
+def zero_list_plan(tensors, n_groups: int = 1):
+    """(zero_list, table as a bytearray).  The caller copies the table to the device and sets table_dev."""
+    recs, out = _list_tensors(tensors), zero_list()
+    size = _lib.zero_list_table_bytes(C.cast(recs, _P), len(tensors))
+    if size == 0:
+        raise ZeroError(ZERO_ERR_INVALID, zero_last_error())
+    table = bytearray(size)
+    _check(_lib.zero_list_plan(C.cast(recs, _P), len(tensors), n_groups, (C.c_char * size).from_buffer(table), size,
+                               C.byref(out)))
+    return out, table
+
+
+def zero_list_repoint(tensors, table: bytearray, lst: zero_list) -> None:
+    """Rewrites the table's first lst.grads_bytes bytes for the tensors' present addresses."""
+    recs = _list_tensors(tensors)
+    _check(_lib.zero_list_repoint(C.cast(recs, _P), len(tensors), (C.c_char * len(table)).from_buffer(table),
+                                  len(table), C.byref(lst)))
+
+
+def zero_list_grad_sqnorm_workspace_bytes(lst: zero_list) -> int:
+    return int(_lib.zero_list_grad_sqnorm_workspace_bytes(C.byref(lst)))
+
+
+def zero_list_grad_sqnorm(lst: zero_list, ws, ws_bytes: int, sqnorm_out, nonfinite_out, stream=None) -> None:
+    _check(_lib.zero_list_grad_sqnorm(C.byref(lst), _buf(ws, ws_bytes), ws_bytes, _buf(sqnorm_out, 8),
+                                      _buf(nonfinite_out, 4), _stream(stream)))
+
+
+def _group_hparams(lst: zero_list, hparams):
+    """The hparams array, after checking that it holds one entry for each group."""
+    if len(hparams) != lst.n_groups:
+        raise ValueError(f"{len(hparams)} hyper-parameter sets for {lst.n_groups} groups")
+    return hparams
+
+
+def zero_list_adamw_step(lst: zero_list, hparams, stream=None) -> None:
+    _check(_lib.zero_list_adamw_step(C.byref(lst), _group_hparams(lst, hparams), _stream(stream)))
+
+
+def zero_list_adamw8_step(lst: zero_list, hparams, seed: int, stream=None) -> None:
+    _check(_lib.zero_list_adamw8_step(C.byref(lst), _group_hparams(lst, hparams), seed, _stream(stream)))
+
+
+def zero_list_decision_dev(rank_sqnorms, rank_flags, n_ranks: int, max_norm: float, hparams, state, groups,
+                           stream=None) -> None:
+    k = max(n_ranks, 0)
+    _check(_lib.zero_list_decision_dev(_buf(rank_sqnorms, 8 * k), _buf(rank_flags, 4 * k), n_ranks, max_norm, hparams,
+                                       len(hparams), _buf(state, _STATE), _buf(groups, 48 * len(hparams)),
+                                       _stream(stream)))
+
+
+def zero_list_adamw_step_dev(lst: zero_list, state, groups, stream=None) -> None:
+    _check(_lib.zero_list_adamw_step_dev(C.byref(lst), _buf(state, _STATE), _buf(groups, 48 * lst.n_groups),
+                                         _stream(stream)))
+
+
+def zero_list_adamw8_step_dev(lst: zero_list, state, groups, seed: int, stream=None) -> None:
+    _check(_lib.zero_list_adamw8_step_dev(C.byref(lst), _buf(state, _STATE), _buf(groups, 48 * lst.n_groups), seed,
+                                          _stream(stream)))
+
+
+def zero_list_state8_pack(from32: zero_list, to8: zero_list, stream=None) -> None:
+    _check(_lib.zero_list_state8_pack(C.byref(from32), C.byref(to8), _stream(stream)))
+
+
+def zero_list_state8_unpack(from8: zero_list, to32: zero_list, stream=None) -> None:
+    _check(_lib.zero_list_state8_unpack(C.byref(from8), C.byref(to32), _stream(stream)))
 
 
 def read_step_state(state_tensor) -> dict:

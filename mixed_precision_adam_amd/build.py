@@ -12,6 +12,7 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "zero_shard.hip")
+LIST_SRC = os.path.join(HERE, "csrc", "zero_list.hip")
 LIB = os.path.join(HERE, "libzero_shard.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CLANG = "/opt/rocm/llvm/bin/clang++"
@@ -58,12 +59,15 @@ def _run(cmd) -> str:
 def build(verbose: bool = False) -> str:
     """Compile the library (always rebuilds) and return its path."""
     tlib = torch_lib_dir()
-    obj = LIB + ".o"
     tmp = LIB + ".tmp"
-    log = _run([HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-c", "-o", obj, SRC])
-    log += _run([CLANG, "-shared", "-o", tmp, obj, "-L", tlib, "-l:libamdhip64.so", f"-Wl,-rpath,{tlib}",
+    objs, log = [], ""
+    for src in (SRC, LIST_SRC):
+        objs.append(f"{LIB}.{os.path.basename(src)}.o")
+        log += _run([HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-c", "-o", objs[-1], src])
+    log += _run([CLANG, "-shared", "-o", tmp, *objs, "-L", tlib, "-l:libamdhip64.so", f"-Wl,-rpath,{tlib}",
                  "-Wl,--no-undefined", "-lm"])
-    os.remove(obj)
+    for obj in objs:
+        os.remove(obj)
     if verbose and log:
         print(log)
     os.replace(tmp, LIB)

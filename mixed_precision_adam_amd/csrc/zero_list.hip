@@ -1,0 +1,926 @@
+// zero_list.hip -- the norm, the update and the 8-bit state over lists of
+// tensors (include/zero_shard.h, "lists of tensors"), for CDNA4 (gfx950).
+//
+// Every kernel here streams HBM: nothing is a contraction.  A list is a table
+// in device memory: one 64-byte descriptor per tensor, then one 8-byte entry
+// (tensor, chunk of the tensor) per workgroup of the norm, then one per
+// workgroup of the update, so a workgroup finds its work with two dependent
+// scalar loads whatever the number of tensors, and one launch covers the list.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "zero_common.h"
+
+#pragma clang fp contract(off)
+
+namespace {
+
+using namespace zero_detail;
+
+// ------------------------------------------------------------------ the table
+
+struct Desc {
+  const void* grad;
+  void* param;
+  float* state;  // master (arrays), tiles (tiled, 8-bit)
+  float* m;
+  float* v;
+  int64_t numel;
+  int64_t block0;  // number of the tensor's first block of ZERO_STATE8_BLOCK elements in the list
+  uint8_t gdt, pdt, layout, group;
+  uint32_t reserved;
+};
+static_assert(sizeof(Desc) == 64, "one scalar load of 16 dwords");
+
+struct Entry {
+  uint32_t tensor, chunk;
+};
+
+constexpr int64_t kMaxTensorNumel = int64_t(1) << 40;
+constexpr int64_t kMaxNormBlocks = int64_t(1) << 23;  // one launch: its threads are counted in 32 bits
+constexpr int64_t kMaxUpdateBlocks = int64_t(1) << 30;
+// Elements per workgroup.
+constexpr int64_t kNormPer = 16384;
+constexpr int64_t kTile8 = ZERO_STATE8_TILE;
+constexpr int kBlock8 = ZERO_STATE8_BLOCK;
+constexpr int64_t kTile8Blocks = kTile8 / kBlock8;
+constexpr int64_t kTile8Bytes = 6 * kTile8 + 8 * kTile8Blocks;
+static_assert(kTile8Bytes % 128 == 0, "tiles keep the cache lines of their parts whole");
+
+int64_t elem_bytes(int dt) { return dt == ZERO_FP32 ? 4 : 2; }
+bool list_dtype_ok(int dt) { return dtype_ok(dt) || dt == ZERO_FP32; }
+
+bool off(const void* p, uintptr_t align) { return (reinterpret_cast<uintptr_t>(p) & (align - 1)) != 0; }
+
+uint64_t fold(uint64_t h, uint64_t x) {  // FNV-1a over the bytes of x
+  for (int k = 0; k < 64; k += 8) h = (h ^ ((x >> k) & 0xFFu)) * 0x100000001B3ull;
+  return h;
+}
+constexpr uint64_t kFoldStart = 0xCBF29CE484222325ull;
+
+uint64_t list_check(const zero_list& l) {
+  uint64_t h = kFoldStart;
+  for (int64_t x : {l.table_bytes, l.grads_bytes, l.numel, l.norm_blocks, l.update_blocks, l.norm_offset,
+                    l.update_offset, static_cast<int64_t>(l.shape), static_cast<int64_t>(l.n_tensors),
+                    static_cast<int64_t>(l.n_groups), static_cast<int64_t>(l.state), static_cast<int64_t>(l.flags)})
+    h = fold(h, static_cast<uint64_t>(x));
+  return h;
+}
+
+// Sizes of the table's parts; false if a size or layout is out of range.
+bool table_shape(const char* fn, const zero_list_tensor* t, int32_t n, zero_list* out) {
+  if (n < 0 || (n > 0 && !t)) {
+    fail(ZERO_ERR_INVALID, "%s: bad tensor list (n_tensors=%d)", fn, n);
+    return false;
+  }
+  zero_list l{};
+  l.n_tensors = n;
+  l.shape = fold(kFoldStart, static_cast<uint64_t>(n));
+  for (int32_t k = 0; k < n; ++k) {
+    if (t[k].numel < 0 || t[k].numel > kMaxTensorNumel) {
+      fail(ZERO_ERR_INVALID, "%s: tensor %d: numel %lld out of range", fn, k, static_cast<long long>(t[k].numel));
+      return false;
+    }
+    if (t[k].layout < ZERO_STATE_NONE || t[k].layout > ZERO_STATE_8BIT) {
+      fail(ZERO_ERR_INVALID, "%s: tensor %d: unknown state layout %d", fn, k, t[k].layout);
+      return false;
+    }
+    const int32_t state = t[k].layout == ZERO_STATE_NONE ? 0 : t[k].layout == ZERO_STATE_8BIT ? 8 : 32;
+    if (k > 0 && state != l.state) {
+      fail(ZERO_ERR_INVALID, "%s: tensor %d: one list holds one kind of state (none, fp32 or 8-bit)", fn, k);
+      return false;
+    }
+    l.state = state;
+    l.shape = fold(l.shape, static_cast<uint64_t>(t[k].numel));
+    l.numel += t[k].numel;
+    l.norm_blocks += ceil_div(t[k].numel, kNormPer);
+    if (state != 0) l.update_blocks += ceil_div(t[k].numel, state == 8 ? kTile8 : kTile);
+    if (l.numel > kMaxPsi || l.norm_blocks > kMaxNormBlocks || l.update_blocks > kMaxUpdateBlocks) {
+      fail(ZERO_ERR_INVALID, "%s: the list is too large", fn);
+      return false;
+    }
+  }
+  l.grads_bytes = static_cast<int64_t>(n) * sizeof(Desc);
+  l.norm_offset = l.grads_bytes;
+  l.update_offset = l.norm_offset + l.norm_blocks * static_cast<int64_t>(sizeof(Entry));
+  l.table_bytes = l.update_offset + l.update_blocks * static_cast<int64_t>(sizeof(Entry));
+  if (l.table_bytes == 0) l.table_bytes = sizeof(Desc);  // an empty list still has a table
+  *out = l;
+  return true;
+}
+
+struct Range {
+  uintptr_t lo, hi;
+  bool written;
+  int32_t tensor;
+};
+
+// Checks one tensor and collects the memory it covers.
+int check_tensor(const char* fn, const zero_list_tensor& t, int32_t k, int32_t n_groups, std::vector<Range>* ranges,
+                 int32_t* flags) {
+  if (!list_dtype_ok(t.gdt)) return fail(ZERO_ERR_INVALID, "%s: tensor %d: unknown gradient dtype %d", fn, k, t.gdt);
+  if (!list_dtype_ok(t.pdt)) return fail(ZERO_ERR_INVALID, "%s: tensor %d: unknown parameter dtype %d", fn, k, t.pdt);
+  if (t.group < 0 || t.group >= n_groups)
+    return fail(ZERO_ERR_INVALID, "%s: tensor %d: group %d outside [0, %d)", fn, k, t.group, n_groups);
+  if (off(t.grad, elem_bytes(t.gdt)) || off(t.param, elem_bytes(t.pdt)))
+    return fail(ZERO_ERR_INVALID, "%s: tensor %d: gradient or parameter not aligned to its element size", fn, k);
+  const bool arrays = t.layout == ZERO_STATE_ARRAYS;
+  if (!arrays && (t.m || t.v))
+    return fail(ZERO_ERR_INVALID, "%s: tensor %d: m and v belong to separate arrays only", fn, k);
+  if (t.layout == ZERO_STATE_NONE && t.state)
+    return fail(ZERO_ERR_INVALID, "%s: tensor %d: a state without a layout", fn, k);
+  if ((t.layout == ZERO_STATE_TILED || t.layout == ZERO_STATE_8BIT) && t.numel > 0 && !t.state)
+    return fail(ZERO_ERR_INVALID, "%s: tensor %d: NULL state", fn, k);
+  if (arrays ? off(t.state, 4) || off(t.m, 4) || off(t.v, 4) : off(t.state, 16))
+    return fail(ZERO_ERR_INVALID, "%s: tensor %d: misaligned state", fn, k);
+  if (t.numel == 0) return ZERO_OK;
+  if (!t.param) *flags &= ~ZERO_LIST_HAS_PARAMS;
+  if (!t.state || (arrays && (!t.m || !t.v))) *flags &= ~ZERO_LIST_WHOLE_STATE;
+  int64_t state_bytes = 4 * t.numel;
+  if (t.layout == ZERO_STATE_TILED) state_bytes = 4 * zero_state_tiled_numel(t.numel);
+  if (t.layout == ZERO_STATE_8BIT) state_bytes = zero_state8_bytes(t.numel);
+  const struct {
+    const void* p;
+    int64_t bytes;
+    bool written;
+  } parts[] = {{t.grad, t.numel * elem_bytes(t.gdt), false},
+               {t.param, t.numel * elem_bytes(t.pdt), true},
+               {t.state, state_bytes, true},
+               {t.m, 4 * t.numel, true},
+               {t.v, 4 * t.numel, true}};
+  for (const auto& part : parts) {
+    if (!part.p) continue;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(part.p);
+    if (lo + static_cast<uintptr_t>(part.bytes) < lo)
+      return fail(ZERO_ERR_INVALID, "%s: tensor %d: a buffer passes the end of the address space", fn, k);
+    ranges->push_back({lo, lo + static_cast<uintptr_t>(part.bytes), part.written, k});
+  }
+  return ZERO_OK;
+}
+
+// Two tensors of a list run on workgroups in any order: nothing that one
+// writes may be another's.
+int check_overlap(const char* fn, std::vector<Range>* ranges) {
+  std::sort(ranges->begin(), ranges->end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t read_end = 0, write_end = 0;
+  for (const Range& r : *ranges) {
+    if (r.lo < write_end || (r.written && r.lo < read_end))
+      return fail(ZERO_ERR_INVALID, "%s: tensor %d: a buffer overlaps one that the update writes", fn, r.tensor);
+    (r.written ? write_end : read_end) = std::max(r.written ? write_end : read_end, r.hi);
+  }
+  return ZERO_OK;
+}
+
+// Checks the tensors and writes their descriptors; *flags receives ZERO_LIST_*.
+int write_descs(const char* fn, const zero_list_tensor* t, int32_t n, int32_t n_groups, Desc* out, int32_t* flags) {
+  std::vector<Range> ranges;
+  ranges.reserve(5 * static_cast<size_t>(n));
+  *flags = ZERO_LIST_HAS_PARAMS | ZERO_LIST_WHOLE_STATE;
+  for (int32_t k = 0; k < n; ++k) {
+    const int rc = check_tensor(fn, t[k], k, n_groups, &ranges, flags);
+    if (rc != ZERO_OK) return rc;
+  }
+  const int rc = check_overlap(fn, &ranges);
+  if (rc != ZERO_OK) return rc;
+  int64_t block0 = 0;
+  for (int32_t k = 0; k < n; ++k) {
+    Desc d{};
+    d.grad = t[k].grad;
+    d.param = t[k].param;
+    d.state = static_cast<float*>(t[k].state);
+    d.m = t[k].m;
+    d.v = t[k].v;
+    if (t[k].layout == ZERO_STATE_TILED && d.state) {
+      d.m = d.state + kTile;
+      d.v = d.state + 2 * kTile;
+    }
+    d.numel = t[k].numel;
+    d.block0 = block0;
+    d.gdt = static_cast<uint8_t>(t[k].gdt);
+    d.pdt = static_cast<uint8_t>(t[k].pdt);
+    d.layout = static_cast<uint8_t>(t[k].layout);
+    d.group = static_cast<uint8_t>(t[k].group);
+    std::memcpy(out + k, &d, sizeof d);
+    block0 += ceil_div(t[k].numel, kTile8) * kTile8Blocks;
+  }
+  return ZERO_OK;
+}
+
+void write_entries(const zero_list_tensor* t, int32_t n, int64_t per, char* out) {
+  for (int32_t k = 0; k < n; ++k)
+    for (int64_t c = 0, chunks = ceil_div(t[k].numel, per); c < chunks; ++c) {
+      const Entry e{static_cast<uint32_t>(k), static_cast<uint32_t>(c)};
+      std::memcpy(out, &e, sizeof e);
+      out += sizeof e;
+    }
+}
+
+// A planned list with its table in place.
+int list_ok(const char* fn, const zero_list* l) {
+  if (!l) return fail(ZERO_ERR_INVALID, "%s: list NULL", fn);
+  if (l->check != list_check(*l)) return fail(ZERO_ERR_INVALID, "%s: the list was not planned", fn);
+  if (l->n_tensors > 0 && (!l->table_dev || !aligned16(l->table_dev)))
+    return fail(ZERO_ERR_INVALID, "%s: the list's device table is NULL or not 16-byte aligned", fn);
+  return ZERO_OK;
+}
+
+// ------------------------------------------------------------------ gradients and parameters
+
+// A descriptor's addresses are global memory: said so, the compiler uses global
+// (not flat) accesses, which do not also wait for LDS.
+#define GLOBAL __attribute__((address_space(1)))
+typedef GLOBAL float* gfloat;
+typedef GLOBAL uint8_t* gbyte;
+typedef GLOBAL uint16_t* gu16;
+
+// Vectors of tensors that start anywhere: the hardware takes any element
+// alignment in one access (global memory in unaligned mode, the default).
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ f32x4 load4(gfloat p) {
+  return __builtin_nontemporal_load(reinterpret_cast<GLOBAL f32x4_any*>(p));
+}
+__device__ __forceinline__ void store4(gfloat p, f32x4 x) {
+  __builtin_nontemporal_store(static_cast<f32x4_any>(x), reinterpret_cast<GLOBAL f32x4_any*>(p));
+}
+
+__device__ __forceinline__ float widen_any(uint32_t h, int dt) {
+  return dt == ZERO_BF16 ? widen<ZERO_BF16>(h) : widen<ZERO_FP16>(h);
+}
+
+// Four consecutive gradients, as they lie (16-bit formats: in the lower half).
+__device__ __forceinline__ u32x4 load_grad4(const void* grad, int dt, int64_t e) {
+  if (dt == ZERO_FP32) return __builtin_nontemporal_load((GLOBAL u32x4_any*)((gfloat)grad + e));
+  const u32x2 w = __builtin_nontemporal_load((GLOBAL u32x2_any*)((gu16)grad + e));
+  return u32x4{w[0], w[1], 0u, 0u};
+}
+
+__device__ __forceinline__ f32x4 widen4(u32x4 w, int dt) {
+  if (dt == ZERO_FP32) return __builtin_bit_cast(f32x4, w);
+  if (dt == ZERO_BF16)
+    return f32x4{widen<ZERO_BF16>(w[0] & 0xFFFFu), widen<ZERO_BF16>(w[0] >> 16), widen<ZERO_BF16>(w[1] & 0xFFFFu),
+                 widen<ZERO_BF16>(w[1] >> 16)};
+  return f32x4{widen<ZERO_FP16>(w[0] & 0xFFFFu), widen<ZERO_FP16>(w[0] >> 16), widen<ZERO_FP16>(w[1] & 0xFFFFu),
+               widen<ZERO_FP16>(w[1] >> 16)};
+}
+
+__device__ __forceinline__ float load_grad1(const void* grad, int dt, int64_t e) {
+  if (dt == ZERO_FP32) return ((gfloat)grad)[e];
+  return widen_any(((gu16)grad)[e], dt);
+}
+
+__device__ __forceinline__ void store_param4(void* param, int dt, int64_t e, f32x4 p) {
+  if (dt == ZERO_FP32) {
+    store4((gfloat)param + e, p);
+    return;
+  }
+  u32x2_any q;
+  if (dt == ZERO_BF16) {
+    q[0] = narrow<ZERO_BF16>(p[0]) | (narrow<ZERO_BF16>(p[1]) << 16);
+    q[1] = narrow<ZERO_BF16>(p[2]) | (narrow<ZERO_BF16>(p[3]) << 16);
+  } else {
+    q[0] = narrow<ZERO_FP16>(p[0]) | (narrow<ZERO_FP16>(p[1]) << 16);
+    q[1] = narrow<ZERO_FP16>(p[2]) | (narrow<ZERO_FP16>(p[3]) << 16);
+  }
+  __builtin_nontemporal_store(q, (GLOBAL u32x2_any*)((gu16)param + e));
+}
+
+__device__ __forceinline__ void store_param1(void* param, int dt, int64_t e, float p) {
+  if (dt == ZERO_FP32) {
+    ((gfloat)param)[e] = p;
+  } else {
+    const uint32_t q = dt == ZERO_BF16 ? narrow<ZERO_BF16>(p) : narrow<ZERO_FP16>(p);
+    ((gu16)param)[e] = static_cast<uint16_t>(q);
+  }
+}
+
+// ------------------------------------------------------------------ scalars
+
+// Scalars of every group by value (host form) or from the device.
+struct GroupTable {
+  AdamScalars s[ZERO_LIST_MAX_GROUPS];
+};
+
+__device__ __forceinline__ bool group_scalars(const GroupTable& host, const zero_step_state* st,
+                                              const zero_group_scalars* groups, int group, AdamScalars* out) {
+  if (st == nullptr) {
+    *out = host.s[group];
+    return true;
+  }
+  if (st->skip) return false;
+  const float* s = groups[group].scalars;
+  *out = AdamScalars{s[0], s[1], s[2], s[3], s[4], s[5], s[6], s[7], s[8]};
+  return true;
+}
+
+// ------------------------------------------------------------------ norm
+
+__device__ __forceinline__ void square(float x, double& acc, uint32_t& bad) {
+  const double d = static_cast<double>(x);
+  acc = acc + d * d;  // exact square: at most 2·24 significant bits
+  bad |= (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u ? 1u : 0u;
+}
+
+// Workgroup b sums the squares of one chunk of one tensor's gradients.
+__global__ __launch_bounds__(kBlock) void list_sqnorm_kernel(const Desc* __restrict__ descs,
+                                                             const Entry* __restrict__ entries,
+                                                             double* __restrict__ part_sum,
+                                                             uint32_t* __restrict__ part_bad) {
+  const Entry en = entries[blockIdx.x];
+  const Desc d = descs[en.tensor];
+  double acc = 0.0;
+  uint32_t bad = 0;
+  if (d.grad != nullptr) {
+    const int64_t lo = static_cast<int64_t>(en.chunk) * kNormPer;
+    const int64_t hi = lo + kNormPer < d.numel ? lo + kNormPer : d.numel;
+    for (int64_t e = lo + 4 * static_cast<int64_t>(threadIdx.x); e < hi; e += 4 * kBlock) {
+      if (e + 4 <= hi) {
+        const f32x4 x = widen4(load_grad4(d.grad, d.gdt, e), d.gdt);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) square(x[c], acc, bad);
+      } else {
+        for (int64_t i = e; i < hi; ++i) square(load_grad1(d.grad, d.gdt, i), acc, bad);
+      }
+    }
+  }
+  block_reduce(acc, bad);
+  if (threadIdx.x == 0) {
+    part_sum[blockIdx.x] = acc;
+    part_bad[blockIdx.x] = bad;
+  }
+}
+
+// ------------------------------------------------------------------ AdamW, fp32 state
+
+// One 256-thread workgroup per 1024 elements of a tensor, thread t owning
+// elements 4t .. 4t+3, as in the flat tiled update.  Both state layouts are
+// the same addresses but for the distance of two chunks: 1024 floats (arrays)
+// or a whole tile of [master | m | v].
+__global__ __launch_bounds__(kBlock) void list_adamw_kernel(const Desc* __restrict__ descs,
+                                                            const Entry* __restrict__ entries, GroupTable host,
+                                                            const zero_step_state* __restrict__ st,
+                                                            const zero_group_scalars* __restrict__ groups) {
+  const Entry en = entries[xcd_grouped(blockIdx.x, gridDim.x)];
+  const Desc d = descs[en.tensor];
+  if (d.grad == nullptr) return;
+  const int64_t at = static_cast<int64_t>(en.chunk) * (d.layout == ZERO_STATE_TILED ? 3 * kTile : kTile) +
+                     4 * static_cast<int64_t>(threadIdx.x);
+  const int64_t e = static_cast<int64_t>(en.chunk) * kTile + 4 * static_cast<int64_t>(threadIdx.x);
+  const gfloat mp = (gfloat)d.state + at, mm = (gfloat)d.m + at, mv = (gfloat)d.v + at;
+  AdamScalars s;
+  if (e + 4 <= d.numel) {
+    const u32x4 g4 = load_grad4(d.grad, d.gdt, e);
+    f32x4 p = load4(mp), m = load4(mm), v = load4(mv);
+    if (!group_scalars(host, st, groups, d.group, &s)) return;
+    const f32x4 g = widen4(g4, d.gdt);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float pc = p[c], mc = m[c], vc = v[c];
+      adam_element(g[c], pc, mc, vc, s);
+      p[c] = pc;
+      m[c] = mc;
+      v[c] = vc;
+    }
+    store4(mp, p);
+    store4(mm, m);
+    store4(mv, v);
+    store_param4(d.param, d.pdt, e, p);
+  } else if (e < d.numel) {
+    if (!group_scalars(host, st, groups, d.group, &s)) return;
+    for (int64_t i = e; i < d.numel; ++i) {
+      const int64_t k = i - e;
+      float p = mp[k], m = mm[k], v = mv[k];
+      adam_element(load_grad1(d.grad, d.gdt, i), p, m, v, s);
+      mp[k] = p;
+      mm[k] = m;
+      mv[k] = v;
+      store_param1(d.param, d.pdt, i, p);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ 8-bit moments
+
+// Hash of a block's number: SplitMix64's output function (Steele, Lea & Flood
+// 2014).  Its arguments are the same for a whole wavefront.
+__host__ __device__ __forceinline__ uint64_t mix64(uint64_t z) {
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  return z ^ (z >> 31);
+}
+constexpr uint64_t kGolden = 0x9E3779B97F4A7C15ull;
+constexpr uint32_t kWeyl = 0x9E3779B9u;
+
+constexpr float kTopM = 448.0f, kTopV = 1.875f;
+constexpr float kSmallestPeak = 0x1p-110f;
+
+// What four codes stand for, without their scale.  An m code is an OCP e4m3
+// number; a v code is the top of an fp32 pattern whose exponent lies 96 lower
+// (its subnormals are fp32's).
+__device__ __forceinline__ f32x4 decode_m(uint32_t c) {
+  const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c), false);
+  const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c), true);
+  return f32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+__device__ __forceinline__ f32x4 decode_v(uint32_t c) {
+  f32x4 x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(((c >> (8 * k)) & 0xFFu) << 20) * 0x1p96f;
+  return x;
+}
+
+// Codes from positions: `low` brings a scaled value down to where its code is
+// the top bits of the fp32 pattern, subnormals included; adding the dither
+// (20 bits: the part of a step that is cut off) rounds up with its
+// probability.
+__device__ __forceinline__ uint32_t code_m(float m, float inv, uint32_t add) {
+  const uint32_t bits = __float_as_uint((fabsf(m) * inv) * 0x1p-120f);
+  const uint32_t c = (bits + add) >> 20;
+  return (c < 126u ? c : 126u) | ((__float_as_uint(m) >> 24) & 0x80u);
+}
+__device__ __forceinline__ uint32_t code_v(float v, float inv, bool some, uint32_t add) {
+  const uint32_t bits = __float_as_uint((fabsf(v) * inv) * 0x1p-96f);
+  uint32_t c = (bits + add) >> 20;
+  c = c < 255u ? c : 255u;
+  return c == 0u && some && v > 0.0f ? 1u : c;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) {
+    const uint32_t y = static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), k, 64));
+    x = x > y ? x : y;
+  }
+  return x;
+}
+
+// The codes and scales of one block: lane l of a wavefront holds elements
+// 4l .. 4l+3 (zeros past the tensor's end).  Peaks are compared as integers,
+// so that a NaN outweighs all.  add_m, add_v: the four elements' dithers.
+struct Codes {
+  uint32_t m, v;
+  float scale_m, scale_v;
+};
+__device__ __forceinline__ Codes encode_block(f32x4 m, f32x4 v, u32x4 add_m, u32x4 add_v) {
+  uint32_t pm = 0, pv = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = __float_as_uint(m[k]) & 0x7FFFFFFFu, b = __float_as_uint(v[k]) & 0x7FFFFFFFu;
+    pm = pm > a ? pm : a;
+    pv = pv > b ? pv : b;
+  }
+  const float peak_m = __uint_as_float(wave_max(pm)), peak_v = __uint_as_float(wave_max(pv));
+  const bool some_m = !(peak_m < kSmallestPeak), some_v = !(peak_v < kSmallestPeak);
+  Codes c;
+  c.scale_m = some_m ? peak_m * (1.0f / kTopM) : 0.0f;
+  c.scale_v = some_v ? peak_v * (1.0f / kTopV) : 0.0f;
+  const float inv_m = some_m ? kTopM / peak_m : 0.0f, inv_v = some_v ? kTopV / peak_v : 0.0f;
+  c.m = 0;
+  c.v = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    c.m |= code_m(m[k], inv_m, add_m[k]) << (8 * k);
+    c.v |= code_v(v[k], inv_v, some_v, add_v[k]) << (8 * k);
+  }
+  return c;
+}
+
+// The parts of one tile.
+struct Tile8 {
+  gfloat master;
+  gbyte m, v;
+  gfloat scale_m, scale_v;
+};
+__device__ __forceinline__ Tile8 tile8(float* state, int64_t tile) {
+  const gbyte base = (gbyte)state + tile * kTile8Bytes;
+  return Tile8{(gfloat)base, base + 4 * kTile8, base + 5 * kTile8, (gfloat)(base + 6 * kTile8),
+               (gfloat)(base + 6 * kTile8) + kTile8Blocks};
+}
+
+// The codes of `have` (0 .. 4) elements, one a byte.
+__device__ __forceinline__ void store_codes(gbyte to, uint32_t word, int have) {
+  if (have == 4) {
+    __builtin_nontemporal_store(word, (GLOBAL uint32_t*)to);
+    return;
+  }
+  for (int k = 0; k < have; ++k) to[k] = static_cast<uint8_t>(word >> (8 * k));
+}
+__device__ __forceinline__ uint32_t load_codes(gbyte from, int have) {
+  if (have == 4) return __builtin_nontemporal_load((GLOBAL uint32_t*)from);
+  uint32_t w = 0;
+  for (int k = 0; k < have; ++k) w |= static_cast<uint32_t>(from[k]) << (8 * k);
+  return w;
+}
+
+// One workgroup per tile of 4096 elements, a wavefront taking four blocks of
+// 256 in turn.
+__global__ __launch_bounds__(kBlock) void list_adamw8_kernel(const Desc* __restrict__ descs,
+                                                             const Entry* __restrict__ entries, GroupTable host,
+                                                             uint64_t seed, uint64_t step,
+                                                             const zero_step_state* __restrict__ st,
+                                                             const zero_group_scalars* __restrict__ groups) {
+  const Entry en = entries[xcd_grouped(blockIdx.x, gridDim.x)];
+  const Desc d = descs[en.tensor];
+  if (d.grad == nullptr) return;
+  AdamScalars s;
+  if (!group_scalars(host, st, groups, d.group, &s)) return;
+  if (st != nullptr) step = static_cast<uint64_t>(st->adam_step);
+  const uint64_t base = mix64(seed + kGolden * step);
+  const Tile8 t = tile8(d.state, en.chunk);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int b = wave; b < kTile8Blocks; b += kBlock / 64) {
+    const int64_t first = static_cast<int64_t>(en.chunk) * kTile8 + b * kBlock8;  // the block's first element
+    if (first >= d.numel) return;
+    const int64_t e = first + 4 * lane;
+    const int have = e + 4 <= d.numel ? 4 : e < d.numel ? static_cast<int>(d.numel - e) : 0;
+    const int at = b * kBlock8 + 4 * lane;  // in the tile
+    f32x4 g = {0, 0, 0, 0}, p = {0, 0, 0, 0};
+    if (have == 4) {
+      g = widen4(load_grad4(d.grad, d.gdt, e), d.gdt);
+      p = load4(t.master + at);
+    } else {
+      for (int k = 0; k < have; ++k) {
+        g[k] = load_grad1(d.grad, d.gdt, e + k);
+        p[k] = t.master[at + k];
+      }
+    }
+    f32x4 m = decode_m(load_codes(t.m + at, have)) * t.scale_m[b];
+    f32x4 v = decode_v(load_codes(t.v + at, have)) * t.scale_v[b];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float pk = p[k], mk = m[k], vk = v[k];
+      adam_element(g[k], pk, mk, vk, s);
+      p[k] = k < have ? pk : 0.0f;
+      m[k] = k < have ? mk : 0.0f;
+      v[k] = k < have ? vk : 0.0f;
+    }
+    const uint32_t key = static_cast<uint32_t>(mix64(base + kGolden * static_cast<uint64_t>(
+        d.block0 + static_cast<int64_t>(en.chunk) * kTile8Blocks + b + 1)));
+    u32x4 r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = key + (4u * static_cast<uint32_t>(lane) + k) * kWeyl;
+    const Codes c = encode_block(m, v, r >> 12, r & 0xFFFFFu);
+    store_codes(t.m + at, c.m, have);
+    store_codes(t.v + at, c.v, have);
+    if (have == 4) {
+      store4(t.master + at, p);
+      store_param4(d.param, d.pdt, e, p);
+    } else {
+      for (int k = 0; k < have; ++k) {
+        t.master[at + k] = p[k];
+        store_param1(d.param, d.pdt, e + k, p[k]);
+      }
+    }
+    if (lane == 0) {
+      t.scale_m[b] = c.scale_m;
+      t.scale_v[b] = c.scale_v;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ conversion
+
+// Offset of element e of a tensor's fp32 state; a NULL part reads as zeros and
+// is not written.
+__device__ __forceinline__ int64_t state32_at(const Desc& d, int64_t e) {
+  return d.layout == ZERO_STATE_TILED ? e / kTile * (3 * kTile) + e % kTile : e;
+}
+__device__ __forceinline__ f32x4 load_part(gfloat part, int64_t at, int have) {
+  f32x4 x = {0, 0, 0, 0};
+  if (part == nullptr) return x;
+  if (have == 4) return load4(part + at);
+  for (int k = 0; k < have; ++k) x[k] = part[at + k];
+  return x;
+}
+__device__ __forceinline__ void store_part(gfloat part, int64_t at, int have, f32x4 x) {
+  if (part == nullptr) return;
+  if (have == 4) {
+    store4(part + at, x);
+    return;
+  }
+  for (int k = 0; k < have; ++k) part[at + k] = x[k];
+}
+
+// Workgroups as in list_adamw8_kernel; a group of four elements never straddles
+// two tiles of the fp32 state.
+template <bool PACK>
+__global__ __launch_bounds__(kBlock) void list_state8_kernel(const Desc* __restrict__ descs32,
+                                                             const Desc* __restrict__ descs8,
+                                                             const Entry* __restrict__ entries8) {
+  const Entry en = entries8[xcd_grouped(blockIdx.x, gridDim.x)];
+  const Desc d = descs8[en.tensor], f = descs32[en.tensor];
+  const Tile8 t = tile8(d.state, en.chunk);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int b = wave; b < kTile8Blocks; b += kBlock / 64) {
+    const int64_t first = static_cast<int64_t>(en.chunk) * kTile8 + b * kBlock8;
+    if (first >= d.numel) return;
+    const int64_t e = first + 4 * lane;
+    const int have = e + 4 <= d.numel ? 4 : e < d.numel ? static_cast<int>(d.numel - e) : 0;
+    const int at = b * kBlock8 + 4 * lane;  // in the tile
+    const int64_t at32 = state32_at(f, e);
+    const gfloat fp = (gfloat)f.state, fm = (gfloat)f.m, fv = (gfloat)f.v;
+    if constexpr (PACK) {
+      const f32x4 p = load_part(fp, at32, have), m = load_part(fm, at32, have), v = load_part(fv, at32, have);
+      const u32x4 half = {0x80000u, 0x80000u, 0x80000u, 0x80000u};
+      const Codes c = encode_block(m, v, half, half);
+      store_codes(t.m + at, c.m, have);
+      store_codes(t.v + at, c.v, have);
+      store_part(t.master, at, have, p);
+      if (lane == 0) {
+        t.scale_m[b] = c.scale_m;
+        t.scale_v[b] = c.scale_v;
+      }
+    } else if (have > 0) {
+      store_part(fp, at32, have, load_part(t.master, at, have));
+      store_part(fm, at32, have, decode_m(load_codes(t.m + at, have)) * t.scale_m[b]);
+      store_part(fv, at32, have, decode_v(load_codes(t.v + at, have)) * t.scale_v[b]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ decision
+
+struct GroupHparams {
+  struct {
+    double lr, beta1, beta2, eps, wd;
+  } g[ZERO_LIST_MAX_GROUPS];
+};
+
+// Thread 0 decides; then thread k derives the scalars of group k.
+__global__ __launch_bounds__(64) void list_decision_kernel(const double* __restrict__ sq,
+                                                           const int32_t* __restrict__ flags, int32_t n_ranks,
+                                                           double max_norm, GroupHparams hp, int32_t n_groups,
+                                                           zero_step_state* __restrict__ st,
+                                                           zero_group_scalars* __restrict__ groups) {
+  __shared__ double gscale;
+  __shared__ int64_t t;
+  __shared__ bool taken;
+  if (threadIdx.x == 0) {
+    taken = take_decision(sq, flags, n_ranks, max_norm, st);
+    t = st->adam_step;
+    gscale = st->grad_scale;
+  }
+  __syncthreads();
+  const int k = static_cast<int>(threadIdx.x);
+  if (!taken || k >= n_groups) return;
+  const auto& h = hp.g[k];
+  float out[9];
+  device_scalars(h.lr, h.beta1, h.beta2, h.eps, h.wd, t, gscale, out);
+  for (int i = 0; i < 9; ++i) groups[k].scalars[i] = out[i];
+  if (k == 0)
+    for (int i = 0; i < 9; ++i) st->scalars[i] = out[i];
+}
+static_assert(ZERO_LIST_MAX_GROUPS <= 64, "one wavefront derives every group's scalars");
+
+// ------------------------------------------------------------------ launches
+
+const Desc* descs_of(const zero_list* l) { return static_cast<const Desc*>(l->table_dev); }
+const Entry* entries_of(const zero_list* l, int64_t offset) {
+  return reinterpret_cast<const Entry*>(static_cast<const char*>(l->table_dev) + offset);
+}
+
+// Issues launch(first entry, count) so that no launch covers more than
+// kUpdateElemsPerLaunch elements.
+template <typename F>
+int for_each_list_launch(const zero_list* l, int64_t per, const char* fn, F&& launch) {
+  const int64_t most = kUpdateElemsPerLaunch / per;
+  for (int64_t b = 0; b < l->update_blocks; b += most) {
+    launch(entries_of(l, l->update_offset) + b, dim3(static_cast<unsigned>(std::min(most, l->update_blocks - b))));
+    const int rc = launch_status(fn);
+    if (rc != ZERO_OK) return rc;
+  }
+  return ZERO_OK;
+}
+
+// A list that the update with `state` bits can take.
+int update_list_ok(const char* fn, const zero_list* l, int32_t state) {
+  const int rc = list_ok(fn, l);
+  if (rc != ZERO_OK) return rc;
+  if (l->n_tensors > 0 && l->state != state)
+    return fail(ZERO_ERR_INVALID, "%s: the list holds %s state", fn,
+                l->state == 8 ? "8-bit" : l->state == 32 ? "fp32" : "no");
+  if (!(l->flags & ZERO_LIST_HAS_PARAMS)) return fail(ZERO_ERR_INVALID, "%s: a tensor has no param", fn);
+  if (!(l->flags & ZERO_LIST_WHOLE_STATE)) return fail(ZERO_ERR_INVALID, "%s: a tensor's state is not whole", fn);
+  return ZERO_OK;
+}
+
+int host_scalars(const char* fn, const zero_list* l, const zero_adamw_hparams* hp, GroupTable* out) {
+  if (!hp) return fail(ZERO_ERR_INVALID, "%s: hparams NULL", fn);
+  for (int32_t k = 0; k < l->n_groups; ++k) {
+    const int rc = adam_scalars(fn, hp + k, out->s + k);
+    if (rc != ZERO_OK) return rc;
+  }
+  return ZERO_OK;
+}
+
+int dev_scalars_ok(const char* fn, const zero_step_state* st, const zero_group_scalars* groups) {
+  if (!st || !aligned16(st)) return fail(ZERO_ERR_INVALID, "%s: step state NULL or not 16-byte aligned", fn);
+  if (!groups || !aligned16(groups)) return fail(ZERO_ERR_INVALID, "%s: group scalars NULL or not 16-byte aligned", fn);
+  return ZERO_OK;
+}
+
+int launch_list_adamw(const char* fn, const zero_list* l, const GroupTable& host, const zero_step_state* st,
+                      const zero_group_scalars* groups, void* stream) {
+  return for_each_list_launch(l, kTile, fn, [&](const Entry* first, dim3 grid) {
+    hipLaunchKernelGGL(list_adamw_kernel, grid, dim3(kBlock), 0, static_cast<hipStream_t>(stream), descs_of(l), first,
+                       host, st, groups);
+  });
+}
+
+int launch_list_adamw8(const char* fn, const zero_list* l, const GroupTable& host, uint64_t seed, uint64_t step,
+                       const zero_step_state* st, const zero_group_scalars* groups, void* stream) {
+  return for_each_list_launch(l, kTile8, fn, [&](const Entry* first, dim3 grid) {
+    hipLaunchKernelGGL(list_adamw8_kernel, grid, dim3(kBlock), 0, static_cast<hipStream_t>(stream), descs_of(l), first,
+                       host, seed, step, st, groups);
+  });
+}
+
+int convert(const char* fn, const zero_list* l32, const zero_list* l8, bool pack, void* stream) {
+  int rc = list_ok(fn, l32);
+  if (rc == ZERO_OK) rc = list_ok(fn, l8);
+  if (rc != ZERO_OK) return rc;
+  if (l32->shape != l8->shape || l32->numel != l8->numel || l32->n_tensors != l8->n_tensors)
+    return fail(ZERO_ERR_INVALID, "%s: the two lists' tensors differ in size", fn);
+  if (l32->n_tensors > 0 && (l32->state != 32 || l8->state != 8))
+    return fail(ZERO_ERR_INVALID, "%s: needs a list with fp32 state and one with 8-bit state", fn);
+  return for_each_list_launch(l8, kTile8, fn, [&](const Entry* first, dim3 grid) {
+    if (pack)
+      hipLaunchKernelGGL(list_state8_kernel<true>, grid, dim3(kBlock), 0, static_cast<hipStream_t>(stream),
+                         descs_of(l32), descs_of(l8), first);
+    else
+      hipLaunchKernelGGL(list_state8_kernel<false>, grid, dim3(kBlock), 0, static_cast<hipStream_t>(stream),
+                         descs_of(l32), descs_of(l8), first);
+  });
+}
+
+}  // namespace
+
+// ====================================================================== C ABI
+
+extern "C" {
+
+int64_t zero_state8_bytes(int64_t n) { return n <= 0 || n > kMaxPsi ? 0 : ceil_div(n, kTile8) * kTile8Bytes; }
+
+int64_t zero_list_table_bytes(const zero_list_tensor* tensors, int32_t n_tensors) {
+  zero_list l;
+  return table_shape("zero_list_table_bytes", tensors, n_tensors, &l) ? l.table_bytes : 0;
+}
+
+int zero_list_plan(const zero_list_tensor* tensors, int32_t n_tensors, int32_t n_groups, void* table_host,
+                   int64_t table_bytes, zero_list* out) try {
+  const char* fn = "zero_list_plan";
+  if (!out || !table_host) return fail(ZERO_ERR_INVALID, "%s: NULL output", fn);
+  if (n_groups < 1 || n_groups > ZERO_LIST_MAX_GROUPS)
+    return fail(ZERO_ERR_INVALID, "%s: n_groups = %d outside [1, %d]", fn, n_groups, ZERO_LIST_MAX_GROUPS);
+  zero_list l;
+  if (!table_shape(fn, tensors, n_tensors, &l)) return ZERO_ERR_INVALID;
+  if (table_bytes < l.table_bytes)
+    return fail(ZERO_ERR_CAPACITY, "%s: table of %lld bytes, %lld needed", fn, static_cast<long long>(table_bytes),
+                static_cast<long long>(l.table_bytes));
+  std::vector<Desc> descs(static_cast<size_t>(n_tensors));
+  const int rc = write_descs(fn, tensors, n_tensors, n_groups, descs.data(), &l.flags);
+  if (rc != ZERO_OK) return rc;
+  char* table = static_cast<char*>(table_host);
+  std::memset(table, 0, static_cast<size_t>(std::min<int64_t>(l.table_bytes, sizeof(Desc))));
+  if (n_tensors > 0) std::memcpy(table, descs.data(), static_cast<size_t>(l.grads_bytes));
+  write_entries(tensors, n_tensors, kNormPer, table + l.norm_offset);
+  if (l.state != 0) write_entries(tensors, n_tensors, l.state == 8 ? kTile8 : kTile, table + l.update_offset);
+  l.n_groups = n_groups;
+  l.check = list_check(l);
+  *out = l;
+  return ZERO_OK;
+} catch (const std::bad_alloc&) {
+  return fail(ZERO_ERR_CAPACITY, "zero_list_plan: out of host memory");
+}
+
+int zero_list_repoint(const zero_list_tensor* tensors, int32_t n_tensors, void* table_host, int64_t table_bytes,
+                      const zero_list* list) try {
+  const char* fn = "zero_list_repoint";
+  if (!list || !table_host) return fail(ZERO_ERR_INVALID, "%s: NULL list or table", fn);
+  if (list->check != list_check(*list)) return fail(ZERO_ERR_INVALID, "%s: the list was not planned", fn);
+  zero_list l;
+  if (!table_shape(fn, tensors, n_tensors, &l)) return ZERO_ERR_INVALID;
+  if (l.shape != list->shape || l.state != list->state || l.n_tensors != list->n_tensors)
+    return fail(ZERO_ERR_INVALID, "%s: the tensors are not the planned ones", fn);
+  if (table_bytes < l.grads_bytes)
+    return fail(ZERO_ERR_CAPACITY, "%s: table of %lld bytes, %lld needed", fn, static_cast<long long>(table_bytes),
+                static_cast<long long>(l.grads_bytes));
+  std::vector<Desc> descs(static_cast<size_t>(n_tensors));
+  const int rc = write_descs(fn, tensors, n_tensors, list->n_groups, descs.data(), &l.flags);
+  if (rc != ZERO_OK) return rc;
+  if (l.flags != list->flags)
+    return fail(ZERO_ERR_INVALID, "%s: params or state that the plan had are missing (or the reverse)", fn);
+  if (n_tensors > 0) std::memcpy(table_host, descs.data(), static_cast<size_t>(l.grads_bytes));
+  return ZERO_OK;
+} catch (const std::bad_alloc&) {
+  return fail(ZERO_ERR_CAPACITY, "zero_list_repoint: out of host memory");
+}
+
+size_t zero_list_grad_sqnorm_workspace_bytes(const zero_list* list) {
+  if (!list || list->check != list_check(*list)) return 0;
+  const size_t need = 12 * static_cast<size_t>(std::max<int64_t>(list->norm_blocks, 1));
+  return (need + 255) / 256 * 256;
+}
+
+int zero_list_grad_sqnorm(const zero_list* list, void* ws_dev, size_t ws_bytes, double* sqnorm_dev,
+                          int32_t* nonfinite_dev, void* stream) {
+  const char* fn = "zero_list_grad_sqnorm";
+  int rc = list_ok(fn, list);
+  if (rc != ZERO_OK) return rc;
+  if (!sqnorm_dev || !nonfinite_dev || !ws_dev) return fail(ZERO_ERR_INVALID, "%s: NULL output or workspace", fn);
+  if (!aligned16(ws_dev)) return fail(ZERO_ERR_INVALID, "%s: workspace must be 16-byte aligned", fn);
+  if (!aligned8(sqnorm_dev) || off(nonfinite_dev, 4)) return fail(ZERO_ERR_INVALID, "%s: misaligned output", fn);
+  const size_t need = zero_list_grad_sqnorm_workspace_bytes(list);
+  if (ws_bytes < need) return fail(ZERO_ERR_INVALID, "%s: workspace %zu bytes < %zu", fn, ws_bytes, need);
+  double* part_sum = static_cast<double*>(ws_dev);
+  uint32_t* part_bad = reinterpret_cast<uint32_t*>(part_sum + std::max<int64_t>(list->norm_blocks, 1));
+  if (list->norm_blocks > 0) {
+    hipLaunchKernelGGL(list_sqnorm_kernel, dim3(static_cast<unsigned>(list->norm_blocks)), dim3(kBlock), 0,
+                       static_cast<hipStream_t>(stream), descs_of(list), entries_of(list, list->norm_offset), part_sum,
+                       part_bad);
+    rc = launch_status(fn);
+    if (rc != ZERO_OK) return rc;
+  }
+  return zero_sqnorm_reduce(part_sum, part_bad, list->norm_blocks, sqnorm_dev, nonfinite_dev, stream);
+}
+
+int zero_list_adamw_step(const zero_list* list, const zero_adamw_hparams* hp, void* stream) {
+  const char* fn = "zero_list_adamw_step";
+  GroupTable host;
+  int rc = update_list_ok(fn, list, 32);
+  if (rc == ZERO_OK) rc = host_scalars(fn, list, hp, &host);
+  return rc != ZERO_OK ? rc : launch_list_adamw(fn, list, host, nullptr, nullptr, stream);
+}
+
+int zero_list_adamw_step_dev(const zero_list* list, const zero_step_state* state_dev,
+                             const zero_group_scalars* groups_dev, void* stream) {
+  const char* fn = "zero_list_adamw_step_dev";
+  int rc = update_list_ok(fn, list, 32);
+  if (rc == ZERO_OK) rc = dev_scalars_ok(fn, state_dev, groups_dev);
+  return rc != ZERO_OK ? rc : launch_list_adamw(fn, list, GroupTable{}, state_dev, groups_dev, stream);
+}
+
+int zero_list_adamw8_step(const zero_list* list, const zero_adamw_hparams* hp, uint64_t seed, void* stream) {
+  const char* fn = "zero_list_adamw8_step";
+  GroupTable host;
+  int rc = update_list_ok(fn, list, 8);
+  if (rc == ZERO_OK) rc = host_scalars(fn, list, hp, &host);
+  if (rc != ZERO_OK) return rc;
+  for (int32_t k = 0; k < list->n_groups; ++k) {
+    if (!(hp[k].eps >= 1e-16)) return fail(ZERO_ERR_INVALID, "%s: group %d: eps below 1e-16", fn, k);
+    if (hp[k].step != hp[0].step) return fail(ZERO_ERR_INVALID, "%s: the groups' steps differ", fn);
+  }
+  return launch_list_adamw8(fn, list, host, seed, static_cast<uint64_t>(hp[0].step), nullptr, nullptr, stream);
+}
+
+int zero_list_adamw8_step_dev(const zero_list* list, const zero_step_state* state_dev,
+                              const zero_group_scalars* groups_dev, uint64_t seed, void* stream) {
+  const char* fn = "zero_list_adamw8_step_dev";
+  int rc = update_list_ok(fn, list, 8);
+  if (rc == ZERO_OK) rc = dev_scalars_ok(fn, state_dev, groups_dev);
+  return rc != ZERO_OK ? rc : launch_list_adamw8(fn, list, GroupTable{}, seed, 0, state_dev, groups_dev, stream);
+}
+
+int zero_list_decision_dev(const double* rank_sqnorms_dev, const int32_t* rank_flags_dev, int32_t n_ranks,
+                           double max_norm, const zero_adamw_hparams* hp, int32_t n_groups,
+                           zero_step_state* state_dev, zero_group_scalars* groups_dev, void* stream) {
+  const char* fn = "zero_list_decision_dev";
+  if (n_ranks < 1 || !rank_sqnorms_dev || !rank_flags_dev || !hp)
+    return fail(ZERO_ERR_INVALID, "%s: NULL argument or n_ranks < 1", fn);
+  if (n_groups < 1 || n_groups > ZERO_LIST_MAX_GROUPS)
+    return fail(ZERO_ERR_INVALID, "%s: n_groups = %d outside [1, %d]", fn, n_groups, ZERO_LIST_MAX_GROUPS);
+  if (!aligned8(rank_sqnorms_dev) || off(rank_flags_dev, 4)) return fail(ZERO_ERR_INVALID, "%s: misaligned norms", fn);
+  const int rc = dev_scalars_ok(fn, state_dev, groups_dev);
+  if (rc != ZERO_OK) return rc;
+  GroupHparams g{};
+  for (int32_t k = 0; k < n_groups; ++k) {
+    zero_adamw_hparams h = hp[k];
+    h.step = 1;
+    h.grad_scale = 1.0;
+    AdamScalars s;
+    const int rc_k = adam_scalars(fn, &h, &s);
+    if (rc_k != ZERO_OK) return rc_k;
+    g.g[k] = {h.lr, h.beta1, h.beta2, h.eps, h.weight_decay};
+  }
+  hipLaunchKernelGGL(list_decision_kernel, dim3(1), dim3(64), 0, static_cast<hipStream_t>(stream), rank_sqnorms_dev,
+                     rank_flags_dev, n_ranks, max_norm, g, n_groups, state_dev, groups_dev);
+  return launch_status(fn);
+}
+
+int zero_list_state8_pack(const zero_list* from32, const zero_list* to8, void* stream) {
+  return convert("zero_list_state8_pack", from32, to8, true, stream);
+}
+
+int zero_list_state8_unpack(const zero_list* from8, const zero_list* to32, void* stream) {
+  return convert("zero_list_state8_unpack", to32, from8, false, stream);
+}
+
+}  // extern "C"

@@ -16,13 +16,18 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (ZERO_BF16, ZERO_FP16, ZERO_STATE_TILE, read_step_state, zero_adamw_step, zero_adamw_step_dev,
+from . import (ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO_STATE_8BIT, ZERO_STATE_ARRAYS, ZERO_STATE_NONE, ZERO_STATE_TILE,
+               ZERO_STATE_TILED, read_step_state, zero_adamw_step, zero_adamw_step_dev,
                zero_adamw_step_tiled, zero_adamw_step_tiled_dev, zero_bucket_segments, zero_flatten_grads,
                zero_flatten_grads_partials, zero_flatten_grads_sqnorm, zero_flatten_partials_count,
-               zero_flatten_plan, zero_grad_sqnorm, zero_grad_sqnorm_workspace_bytes, zero_shard_layout,
+               zero_flatten_plan, zero_grad_sqnorm, zero_grad_sqnorm_workspace_bytes, zero_list_adamw8_step,
+               zero_list_adamw8_step_dev, zero_list_adamw_step, zero_list_adamw_step_dev, zero_list_decision_dev,
+               zero_list_grad_sqnorm, zero_list_grad_sqnorm_workspace_bytes, zero_list_hparams, zero_list_plan,
+               zero_list_repoint, zero_list_state8_pack, zero_list_state8_unpack, zero_shard_layout,
                zero_sqnorm_reduce, zero_state_tile, zero_state_tiled_numel, zero_state_untile, zero_step_decision,
                zero_step_decision_dev, zero_step_state_init)
 
+_FORMAT = {torch.bfloat16: ZERO_BF16, torch.float16: ZERO_FP16, torch.float32: ZERO_FP32}
 _TORCH16 = {ZERO_BF16: torch.bfloat16, ZERO_FP16: torch.float16}
 
 
@@ -286,6 +291,134 @@ class BucketPipeline:
                                weight_decay=c.weight_decay, stream=stream)
 
     def read(self) -> dict:
+        return read_step_state(self.state)
+
+
+class TensorList:
+    """A planned list of tensors: gradients read and parameters written where they lie, with fp32 state
+    (``state`` tiled, or ``master``/``m``/``v``), 8-bit state (``state8``) or none (norm only).  Every argument is
+    a list with one contiguous GPU tensor per list entry; ``grads`` and ``params`` may hold views at any element
+    offset, and a gradient may be None (no gradient in this step: that tensor is left as it is).  Calls run on
+    the current stream of the tensors' device unless a stream is given; the table, the norm's workspace and the
+    tensors belong to the list, so calls that may overlap in time need lists of their own."""
+
+    def __init__(self, numels, grads=None, params=None, *, state=None, state8=None, master=None, m=None, v=None,
+                 groups=None, n_groups: int = 1):
+        given = [x for x in (grads, params, state, state8, master, m, v) if x is not None]
+        for x in given + ([groups] if groups is not None else []):
+            if len(x) != len(numels):
+                raise ValueError(f"{len(x)} entries for {len(numels)} tensors")
+        devices = {t.device for x in given for t in x if t is not None}
+        if len(devices) > 1 or any(d.type != "cuda" for d in devices):
+            raise ValueError(f"the tensors of a list belong on one GPU, got {sorted(map(str, devices))}")
+        if (state is not None) + (state8 is not None) + any(x is not None for x in (master, m, v)) > 1:
+            raise ValueError("one kind of state: tiled, 8-bit or master/m/v")
+        for x, kinds in ((grads, _FORMAT), (params, _FORMAT), (state, {torch.float32}), (state8, {torch.uint8}),
+                         (master, {torch.float32}), (m, {torch.float32}), (v, {torch.float32})):
+            bad = [t.dtype for t in x or () if t is not None and t.dtype not in kinds]
+            if bad:
+                raise ValueError(f"dtype {bad[0]} where one of {sorted(map(str, kinds))} is needed")
+        layout = (ZERO_STATE_TILED if state is not None else ZERO_STATE_8BIT if state8 is not None else
+                  ZERO_STATE_ARRAYS if any(x is not None for x in (master, m, v)) else ZERO_STATE_NONE)
+        self.device = devices.pop() if devices else torch.device("cuda", torch.cuda.current_device())
+        state = next((x for x in (state, state8, master) if x is not None), None)
+        self._tensors = [dict(numel=n, layout=layout, group=groups[k] if groups is not None else 0,
+                              **{f: x[k] for f, x in (("param", params), ("state", state), ("m", m), ("v", v))
+                                 if x is not None}) for k, n in enumerate(numels)]
+        for t in self._tensors:
+            if t.get("param") is not None:
+                t["pdt"] = _FORMAT[t["param"].dtype]
+        self._point(grads)
+        self.list, self._host = zero_list_plan(self._tensors, n_groups)
+        self.table = torch.frombuffer(self._host, dtype=torch.uint8).to(self.device)
+        self.list.table_dev = self.table.data_ptr()
+        self.ws_bytes = zero_list_grad_sqnorm_workspace_bytes(self.list)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self.state8 = state8 is not None
+
+    def _point(self, grads) -> None:
+        for k, t in enumerate(self._tensors):
+            t["grad"] = None if grads is None else grads[k]
+            if t["grad"] is not None:
+                t["gdt"] = _FORMAT[t["grad"].dtype]
+
+    def set_grads(self, grads) -> None:
+        """Other gradient tensors (or None) for the coming steps: rewrites the table's descriptors, ordered on the
+        current stream."""
+        if len(grads) != len(self._tensors):
+            raise ValueError(f"{len(grads)} gradients for {len(self._tensors)} tensors")
+        bad = [g for g in grads if g is not None and (g.device != self.device or g.dtype not in _FORMAT)]
+        if bad:
+            raise ValueError(f"gradients belong on {self.device} in bf16, fp16 or fp32, got {bad[0].dtype} on "
+                             f"{bad[0].device}")
+        self._point(grads)
+        zero_list_repoint(self._tensors, self._host, self.list)
+        n = self.list.grads_bytes
+        if n:
+            self.table[:n].copy_(torch.frombuffer(self._host, dtype=torch.uint8, count=n))
+
+    def _call(self, fn, *args, stream=None) -> None:
+        if torch.cuda.current_device() == self.device.index:
+            fn(*args, stream)
+        else:  # kernels are launched from the device that holds the tensors
+            with torch.cuda.device(self.device):
+                fn(*args, stream)
+
+    def grad_sqnorm(self, sqnorm_out, nonfinite_out, stream=None) -> None:
+        """fp64 sum of squares and inf/NaN flag over every gradient."""
+        self._call(zero_list_grad_sqnorm, self.list, self.ws, self.ws_bytes, sqnorm_out, nonfinite_out, stream=stream)
+
+    def adamw(self, hparams, stream=None, seed: int = 0) -> None:
+        """The update with host scalars (zero_list_hparams); `seed` sets the rounding of 8-bit moments."""
+        if self.state8:
+            self._call(zero_list_adamw8_step, self.list, hparams, seed, stream=stream)
+        else:
+            self._call(zero_list_adamw_step, self.list, hparams, stream=stream)
+
+    def adamw_dev(self, step_state, group_scalars, stream=None, seed: int = 0) -> None:
+        """The update with the scalars of zero_list_decision_dev."""
+        if self.state8:
+            self._call(zero_list_adamw8_step_dev, self.list, step_state, group_scalars, seed, stream=stream)
+        else:
+            self._call(zero_list_adamw_step_dev, self.list, step_state, group_scalars, stream=stream)
+
+    def pack8(self, target: "TensorList", stream=None) -> None:
+        """This list's fp32 state into the 8-bit state of `target` (a list of the same sizes)."""
+        self._call(zero_list_state8_pack, self.list, target.list, stream=stream)
+
+    def unpack8(self, target: "TensorList", stream=None) -> None:
+        """This list's 8-bit state into the fp32 state of `target`."""
+        self._call(zero_list_state8_unpack, self.list, target.list, stream=stream)
+
+
+class ListDecision:
+    """Device-resident steps over a TensorList: norm, decision (with the scalars of every group) and update are
+    queued back to back with no host round trip, and can be captured in a HIP graph."""
+
+    def __init__(self, tensors: TensorList, cfgs, max_norm: float = 1.0, loss_scale: float = 1.0,
+                 growth_interval: int = 2**31 - 1, seed: int = 0):
+        dev = tensors.device
+        self.tensors, self.max_norm, self.seed = tensors, max_norm, seed
+        self.hparams = zero_list_hparams([dict(lr=c.lr, beta1=c.beta1, beta2=c.beta2, eps=c.eps,
+                                               weight_decay=c.weight_decay) for c in cfgs])
+        if len(self.hparams) != tensors.list.n_groups:
+            raise ValueError(f"{len(self.hparams)} configurations for {tensors.list.n_groups} groups")
+        self.norms = torch.zeros(2, dtype=torch.float64, device=dev)  # square-norm, then its flag
+        self.state = torch.zeros(16, dtype=torch.float64, device=dev)
+        self.groups = torch.zeros(12 * len(self.hparams), dtype=torch.float32, device=dev)
+        with torch.cuda.device(dev):
+            zero_step_state_init(self.state, loss_scale, growth_interval)
+
+    def step(self, stream=None) -> None:
+        """Enqueues one whole step; nothing waits on the host."""
+        sq, flag = self.norms[:1], self.norms[1:].view(torch.int32)
+        self.tensors.grad_sqnorm(sq, flag, stream)
+        self.tensors._call(zero_list_decision_dev, sq, flag, 1, self.max_norm, self.hparams, self.state, self.groups,
+                           stream=stream)
+        self.tensors.adamw_dev(self.state, self.groups, stream, self.seed)
+
+    def read(self) -> dict:
+        """The decided state (synchronizes)."""
         return read_step_state(self.state)
 
 
