@@ -431,7 +431,8 @@ enum {
  * reciprocal of the constant), and x·(448/peak) (1.875/peak) is rounded to a
  * code.  A v that is not zero never takes code 0.  A NaN or infinity in a
  * block makes its scale NaN or infinite: the whole block then reads as not
- * finite (a step whose norm flagged it is to be skipped, as ever).
+ * finite (a step whose norm flagged it is to be skipped, as ever).  Packing
+ * takes the magnitude of a v.
  *   Updates round stochastically: position p between two codes k and k+1 goes
  * to k+1 with probability p - k, so the expected value is the value.  With
  * rounding to nearest the second moment would stand still: a step changes it
@@ -529,10 +530,14 @@ int zero_list_grad_sqnorm(const zero_list* list, void* ws_dev, size_t ws_bytes, 
 int zero_list_adamw_step(const zero_list* list, const zero_adamw_hparams* hp, void* stream);
 
 /* Device.  The same with 8-bit state: the moments are decoded, take
- * zero_adamw_step's operations (the parameter and the master come from the new
- * moments before they are rounded) and are encoded again.  eps >= 1e-16 for
- * every group (a second moment whose block is held as zeros reads as 0).
- * Every group's hp must have the same step, which with seed sets the dither. */
+ * zero_adamw_step's operations bit for bit and are encoded again; master and
+ * parameter come from the new moments before they are rounded.  The step that
+ * the master takes may differ from zero_adamw_step's by 14·2^-24 of itself and
+ * its rounding by one unit (hardware root and reciprocals, 1 ulp each, and
+ * fused products; a second moment below 2^-126 may count as 0 under the root).
+ * eps >= 1e-16 for every group (a second moment whose block is held as zeros
+ * reads as 0).  Every group's hp must have the same step, which with seed sets
+ * the dither. */
 int zero_list_adamw8_step(const zero_list* list, const zero_adamw_hparams* hp, uint64_t seed, void* stream);
 
 /* Scalars of one group on the device: those of zero_step_state. */
