@@ -393,6 +393,9 @@ int zero_adamw_step_tiled_dev(const void* grad_dev, zero_dtype gdt, float* state
  * flattened one 32).  A list can hold whole tensors (data parallelism without
  * sharding) or a rank's pieces of them (zero_shard_layout's segments).  The
  * tensors of a list may differ in size, format, state layout and group.
+ * Calls are made with the device that holds the tensors current.  Host scalars
+ * (zero_list_adamw*_step) are fixed in a captured graph; the _dev forms read
+ * theirs at every replay.
  *
  *   zero_list_plan            checks a list and builds its device table
  *   zero_list_grad_sqnorm     fp64 sum of squares and inf/NaN flag
@@ -556,7 +559,8 @@ int zero_list_decision_dev(const double* rank_sqnorms_dev, const int32_t* rank_f
 
 /* Device.  The updates with the scalars and the Adam step taken from the
  * device (groups_dev[list->n_groups]); when state_dev->skip is set they return
- * without touching memory. */
+ * without touching memory.  With 8-bit state an eps below 1e-16 counts as
+ * 1e-16. */
 int zero_list_adamw_step_dev(const zero_list* list, const zero_step_state* state_dev,
                              const zero_group_scalars* groups_dev, void* stream);
 int zero_list_adamw8_step_dev(const zero_list* list, const zero_step_state* state_dev,

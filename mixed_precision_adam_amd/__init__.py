@@ -450,7 +450,8 @@ def _list_tensors(tensors):
         k = max(n, 0)
         rec.numel, rec.layout, rec.group = n, layout, t.get("group", 0)
         rec.gdt, rec.pdt = t.get("gdt", ZERO_BF16), t.get("pdt", ZERO_BF16)
-        held = {ZERO_STATE_TILED: 4 * zero_state_tiled_numel(k), ZERO_STATE_8BIT: zero_state8_bytes(k)}.get(layout, 4 * k)
+        held = (4 * zero_state_tiled_numel(k) if layout == ZERO_STATE_TILED else
+                zero_state8_bytes(k) if layout == ZERO_STATE_8BIT else 4 * k)
         rec.grad = _buf(t.get("grad"), k * _ELEM.get(rec.gdt, 4))
         rec.param = _buf(t.get("param"), k * _ELEM.get(rec.pdt, 4))
         rec.state, rec.m, rec.v = _buf(t.get("state"), held), _buf(t.get("m"), 4 * k), _buf(t.get("v"), 4 * k)

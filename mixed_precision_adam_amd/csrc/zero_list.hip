@@ -511,10 +511,13 @@ constexpr uint32_t kWeyl = 0x9E3779B9u;
 
 constexpr float kTopM = 448.0f, kTopV = 1.875f;
 constexpr float kSmallestPeak = 0x1p-110f;
+// A second moment whose block is held as zeros reads as 0: eps alone then
+// divides the first.
+constexpr float kLeastEps8 = 1e-16f;
 
-// A wavefront takes kUnits adjacent blocks of a tile, lane l holding elements
+// A wavefront takes U adjacent blocks of a tile, lane l holding elements
 // 4l .. 4l+3 of each, so that every access of a wavefront is one contiguous
-// span; a 256-thread workgroup takes the tile.
+// span.  With U = kUnits a 256-thread workgroup takes the tile.
 constexpr int kUnits = 4;
 static_assert(kTile8 == kUnits * kBlock8 * (kBlock / 64), "four wavefronts cover a tile");
 
@@ -568,25 +571,38 @@ __device__ __forceinline__ uint32_t max_dpp(uint32_t x, uint32_t y) {
 // the lanes are halved, in 4 + 2 + 1 + 3 steps where one value after the
 // other takes 8 x 6.  Group l / 8 of eight lanes ends with the peak of moment
 // (l / 32: m, v) of block peak_unit(l).
-__device__ __forceinline__ int peak_unit(int lane) { return ((lane >> 4) & 1) | ((lane >> 2) & 2); }
+// (One block: lanes 0 .. 31 and 32 .. 63 end with the peaks of m and v.)
+template <int U>
+__device__ __forceinline__ int peak_unit(int lane) {
+  return U == 1 ? 0 : ((lane >> 4) & 1) | ((lane >> 2) & 2);
+}
 __device__ __forceinline__ int peak_lane(int unit) { return ((unit & 1) << 4) | ((unit & 2) << 2); }
-__device__ __forceinline__ uint32_t fold_peaks(const uint32_t (&m)[kUnits], const uint32_t (&v)[kUnits], int lane) {
-  uint32_t r[kUnits], q[2];
+__device__ __forceinline__ uint32_t max_of(uint32_t a, uint32_t b) { return a > b ? a : b; }
+template <int U>
+__device__ __forceinline__ uint32_t fold_peaks(const uint32_t (&m)[U], const uint32_t (&v)[U], int lane) {
+  uint32_t r[U], x;
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {  // lanes 0 .. 31: m, 32 .. 63: v
+  for (int u = 0; u < U; ++u) {  // lanes 0 .. 31: m, 32 .. 63: v
     const auto s = __builtin_amdgcn_permlane32_swap(m[u], v[u], false, false);
-    r[u] = s[0] > s[1] ? s[0] : s[1];
+    r[u] = max_of(s[0], s[1]);
   }
+  if constexpr (U == 1) {
+    const auto s = __builtin_amdgcn_permlane16_swap(r[0], r[0], false, false);
+    x = max_of(s[0], s[1]);
+    x = max_dpp<0x128>(x, x);  // row_ror:8
+  } else {
+    uint32_t q[2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {  // rows of 16: blocks 2u and 2u + 1 in turn
-    const auto s = __builtin_amdgcn_permlane16_swap(r[2 * u], r[2 * u + 1], false, false);
-    q[u] = s[0] > s[1] ? s[0] : s[1];
+    for (int u = 0; u < 2; ++u) {  // rows of 16: blocks 2u and 2u + 1 in turn
+      const auto s = __builtin_amdgcn_permlane16_swap(r[2 * u], r[2 * u + 1], false, false);
+      q[u] = max_of(s[0], s[1]);
+    }
+    const bool upper = (lane & 8) != 0;  // half rows: blocks 0, 1 and 2, 3
+    x = max_dpp<0x128>(upper ? q[1] : q[0], upper ? q[0] : q[1]);
   }
-  const bool upper = (lane & 8) != 0;  // half rows: blocks 0, 1 and 2, 3
-  uint32_t x = max_dpp<0x128>(upper ? q[1] : q[0], upper ? q[0] : q[1]);  // row_ror:8
-  x = max_dpp<0xB1>(x, x);                                                // quad_perm:[1,0,3,2]
-  x = max_dpp<0x4E>(x, x);                                                // quad_perm:[2,3,0,1]
-  return max_dpp<0x141>(x, x);                                            // row_half_mirror
+  x = max_dpp<0xB1>(x, x);      // quad_perm:[1,0,3,2]
+  x = max_dpp<0x4E>(x, x);      // quad_perm:[2,3,0,1]
+  return max_dpp<0x141>(x, x);  // row_half_mirror
 }
 
 __device__ __forceinline__ float read_lane(float x, int lane) {
@@ -597,12 +613,12 @@ __device__ __forceinline__ float read_lane(float x, int lane) {
 // here), and this lane's scale: that of its group's block and moment.  One
 // division serves all eight.  dither(u, k): what element k of block u adds to
 // the positions of m and v.
-template <typename F>
-__device__ __forceinline__ float encode_blocks(const f32x4 (&m)[kUnits], const f32x4 (&v)[kUnits], int lane, F&& dither,
-                                               uint32_t (&cm)[kUnits], uint32_t (&cv)[kUnits]) {
-  uint32_t pm[kUnits], pv[kUnits];
+template <int U, typename F>
+__device__ __forceinline__ float encode_blocks(const f32x4 (&m)[U], const f32x4 (&v)[U], int lane, F&& dither,
+                                               uint32_t (&cm)[U], uint32_t (&cv)[U]) {
+  uint32_t pm[U], pv[U];
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
+  for (int u = 0; u < U; ++u) {
     float a = fabsf(m[u][0]);
     pv[u] = __float_as_uint(v[u][0]);
 #pragma unroll
@@ -613,13 +629,13 @@ __device__ __forceinline__ float encode_blocks(const f32x4 (&m)[kUnits], const f
     }
     pm[u] = __float_as_uint(a);
   }
-  const float peak = __uint_as_float(fold_peaks(pm, pv, lane));
+  const float peak = __uint_as_float(fold_peaks<U>(pm, pv, lane));
   const bool some = !(peak < kSmallestPeak);
   const float scale = some ? peak * (lane < 32 ? 1.0f / kTopM : 1.0f / kTopV) : 0.0f;
   const float inv = some ? (lane < 32 ? kTopM : kTopV) / peak : 0.0f;
   const uint64_t held = __ballot(some);
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
+  for (int u = 0; u < U; ++u) {
     const float inv_m = read_lane(inv, peak_lane(u)), inv_v = read_lane(inv, 32 + peak_lane(u));
     const uint32_t least = static_cast<uint32_t>((held >> (32 + peak_lane(u))) & 1u);
     cm[u] = signs(m[u]);
@@ -677,12 +693,14 @@ __device__ __forceinline__ void store_have(gfloat p, int have, f32x4 x) {
 }
 
 // A wavefront's share of a tile.  FULL: all its elements are the tensor's.
+template <int U>
 struct Share {
+  static_assert(U == 1 || U == 4, "blocks of a wavefront");
   int64_t first;  // its first element in the tensor
   int64_t numel;
   Tile8 t;
-  int wave, lane;
-  __device__ int at(int u) const { return (wave * kUnits + u) * kBlock8 + 4 * lane; }  // in the tile
+  int block, lane;  // its first block in the tile
+  __device__ int at(int u) const { return (block + u) * kBlock8 + 4 * lane; }  // in the tile
   __device__ int64_t elem(int u) const { return first + u * kBlock8 + 4 * lane; }
   template <bool FULL>
   __device__ int have(int u) const {
@@ -691,28 +709,39 @@ struct Share {
     return left >= 4 ? 4 : left > 0 ? static_cast<int>(left) : 0;
   }
   template <bool FULL>
-  __device__ void load_moments(uint32_t (&mc)[kUnits], uint32_t (&vc)[kUnits], f32x4* sm, f32x4* sv) const {
+  __device__ void load_moments(uint32_t (&mc)[U], uint32_t (&vc)[U], float (&sm)[U], float (&sv)[U]) const {
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
+    for (int u = 0; u < U; ++u) {
       mc[u] = load_codes(t.m + at(u), have<FULL>(u));
       vc[u] = load_codes(t.v + at(u), have<FULL>(u));
     }
-    *sm = *reinterpret_cast<GLOBAL f32x4*>(t.scale_m + wave * kUnits);
-    *sv = *reinterpret_cast<GLOBAL f32x4*>(t.scale_v + wave * kUnits);
+    if constexpr (U == 4) {
+      const f32x4 m4 = *(GLOBAL f32x4*)(t.scale_m + block), v4 = *(GLOBAL f32x4*)(t.scale_v + block);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        sm[u] = m4[u];
+        sv[u] = v4[u];
+      }
+    } else {
+      sm[0] = t.scale_m[block];
+      sv[0] = t.scale_v[block];
+    }
   }
   // The lane that holds a block's scale for all of its group writes it.
   __device__ void store_scale(float scale) const {
-    const int u = peak_unit(lane);
-    if ((lane & 7) == 0 && first + u * kBlock8 < numel)
-      (lane < 32 ? t.scale_m : t.scale_v)[wave * kUnits + u] = scale;
+    const int u = peak_unit<U>(lane);
+    if ((lane & (U == 1 ? 31 : 7)) == 0 && first + u * kBlock8 < numel)
+      (lane < 32 ? t.scale_m : t.scale_v)[block + u] = scale;
   }
 };
 
-__device__ __forceinline__ Share share_of(const Desc& d, uint32_t chunk) {
-  Share s;
-  s.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// `part`: which of the tile's kUnits / U workgroups this one is.
+template <int U>
+__device__ __forceinline__ Share<U> share_of(const Desc& d, uint32_t chunk, int part = 0) {
+  Share<U> s;
+  s.block = (part * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * U;
   s.lane = threadIdx.x & 63;
-  s.first = static_cast<int64_t>(chunk) * kTile8 + s.wave * (kUnits * kBlock8);
+  s.first = static_cast<int64_t>(chunk) * kTile8 + s.block * kBlock8;
   s.numel = d.numel;
   s.t = tile8(d.state, chunk);
   return s;
@@ -742,11 +771,11 @@ __device__ __forceinline__ void adam8_element(float g, float& p, float& m, float
 
 // The share's gradients as they lie, and as fp32; its parameters.  One branch
 // on the format each, so that the accesses are issued together.
-template <int DT, bool FULL>
-__device__ __forceinline__ void load_grads(const Desc& d, const Share& w, u32x4 (&g)[kUnits]) {
+template <int U, int DT, bool FULL>
+__device__ __forceinline__ void load_grads(const Desc& d, const Share<U>& w, u32x4 (&g)[U]) {
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int have = w.have<FULL>(u);
+  for (int u = 0; u < U; ++u) {
+    const int have = w.template have<FULL>(u);
     g[u] = u32x4{0, 0, 0, 0};
     if (have == 4) {
       g[u] = load_grad4(d.grad, DT, w.elem(u));
@@ -761,16 +790,16 @@ __device__ __forceinline__ void load_grads(const Desc& d, const Share& w, u32x4 
     }
   }
 }
-template <int DT>
-__device__ __forceinline__ void widen_grads(const u32x4 (&raw)[kUnits], f32x4 (&g)[kUnits]) {
+template <int U, int DT>
+__device__ __forceinline__ void widen_grads(const u32x4 (&raw)[U], f32x4 (&g)[U]) {
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) g[u] = widen4(raw[u], DT);
+  for (int u = 0; u < U; ++u) g[u] = widen4(raw[u], DT);
 }
-template <int DT, bool FULL>
-__device__ __forceinline__ void store_params(const Desc& d, const Share& w, const f32x4 (&p)[kUnits]) {
+template <int U, int DT, bool FULL>
+__device__ __forceinline__ void store_params(const Desc& d, const Share<U>& w, const f32x4 (&p)[U]) {
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int have = w.have<FULL>(u);
+  for (int u = 0; u < U; ++u) {
+    const int have = w.template have<FULL>(u);
     if (have == 4) {
       store_param4(d.param, DT, w.elem(u), p[u]);
     } else {
@@ -779,42 +808,44 @@ __device__ __forceinline__ void store_params(const Desc& d, const Share& w, cons
   }
 }
 
-template <bool FULL>
-__device__ __forceinline__ void adamw8_share(const Desc& d, const Share& w, const GroupTable& host, uint64_t seed,
+template <int U, bool FULL>
+__device__ __forceinline__ void adamw8_share(const Desc& d, const Share<U>& w, const GroupTable& host, uint64_t seed,
                                              uint64_t step, const zero_step_state* st,
                                              const zero_group_scalars* groups) {
-  u32x4 g4[kUnits];
-  f32x4 p[kUnits], g[kUnits], m[kUnits], v[kUnits], sm, sv;
-  uint32_t mc[kUnits], vc[kUnits];
+  u32x4 g4[U];
+  f32x4 p[U], g[U], m[U], v[U];
+  float sm[U], sv[U];
+  uint32_t mc[U], vc[U];
   if (d.gdt() == ZERO_FP32) {
-    load_grads<ZERO_FP32, FULL>(d, w, g4);
+    load_grads<U, ZERO_FP32, FULL>(d, w, g4);
   } else {
-    load_grads<ZERO_BF16, FULL>(d, w, g4);
+    load_grads<U, ZERO_BF16, FULL>(d, w, g4);
   }
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) p[u] = load_have(w.t.master + w.at(u), w.have<FULL>(u));
-  w.load_moments<FULL>(mc, vc, &sm, &sv);
+  for (int u = 0; u < U; ++u) p[u] = load_have(w.t.master + w.at(u), w.template have<FULL>(u));
+  w.template load_moments<FULL>(mc, vc, sm, sv);
   AdamScalars s;  // fetched while the data is on its way
   if (!group_scalars(host, st, groups, d.group(), &s)) return;
+  s.eps = fmaxf(s.eps, kLeastEps8);
   if (st != nullptr) step = static_cast<uint64_t>(st->adam_step);
   const uint64_t base = mix64(seed + kGolden * step);
   const uint64_t block = static_cast<uint64_t>(d.block0 + w.first / kBlock8);
-  uint32_t key[kUnits];
+  uint32_t key[U];
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u)
+  for (int u = 0; u < U; ++u)
     key[u] = static_cast<uint32_t>(mix64(base + kGolden * (block + static_cast<uint64_t>(u) + 1)));
   const uint32_t weyl = 4u * static_cast<uint32_t>(w.lane) * kWeyl;
   const float inv_bc2 = __builtin_amdgcn_rcpf(s.bc2_sqrt);
   if (d.gdt() == ZERO_BF16) {
-    widen_grads<ZERO_BF16>(g4, g);
+    widen_grads<U, ZERO_BF16>(g4, g);
   } else if (d.gdt() == ZERO_FP16) {
-    widen_grads<ZERO_FP16>(g4, g);
+    widen_grads<U, ZERO_FP16>(g4, g);
   } else {
-    widen_grads<ZERO_FP32>(g4, g);
+    widen_grads<U, ZERO_FP32>(g4, g);
   }
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int have = w.have<FULL>(u);
+  for (int u = 0; u < U; ++u) {
+    const int have = w.template have<FULL>(u);
     m[u] = decode_m(mc[u]) * sm[u];
     v[u] = decode_v(vc[u]) * sv[u];
 #pragma unroll
@@ -828,20 +859,20 @@ __device__ __forceinline__ void adamw8_share(const Desc& d, const Share& w, cons
     store_have(w.t.master + w.at(u), have, p[u]);
   }
   if (d.pdt() == ZERO_BF16) {
-    store_params<ZERO_BF16, FULL>(d, w, p);
+    store_params<U, ZERO_BF16, FULL>(d, w, p);
   } else if (d.pdt() == ZERO_FP16) {
-    store_params<ZERO_FP16, FULL>(d, w, p);
+    store_params<U, ZERO_FP16, FULL>(d, w, p);
   } else {
-    store_params<ZERO_FP32, FULL>(d, w, p);
+    store_params<U, ZERO_FP32, FULL>(d, w, p);
   }
   const float scale = encode_blocks(m, v, w.lane, [&](int u, int k) {
     const uint32_t r = key[u] + weyl + static_cast<uint32_t>(k) * kWeyl;
     return u32x2{r >> 12, r & 0xFFFFFu};
   }, mc, vc);
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    store_codes(w.t.m + w.at(u), mc[u], w.have<FULL>(u));
-    store_codes(w.t.v + w.at(u), vc[u], w.have<FULL>(u));
+  for (int u = 0; u < U; ++u) {
+    store_codes(w.t.m + w.at(u), mc[u], w.template have<FULL>(u));
+    store_codes(w.t.v + w.at(u), vc[u], w.template have<FULL>(u));
   }
   w.store_scale(scale);
 }
@@ -853,19 +884,22 @@ __device__ __forceinline__ void adamw8_share(const Desc& d, const Share& w, cons
 // divisions, took 3.3 ms: about 130 issue slots an element where HBM leaves
 // time for 98; now it is 50.  Caps of 3, 4 and 5 wavefronts per SIMD are
 // within 1%.
+template <int U>
 STREAMING_KERNEL void list_adamw8_kernel(const Desc* __restrict__ descs, const Entry* __restrict__ entries,
                                          GroupTable host, uint64_t seed, uint64_t step,
                                          const zero_step_state* __restrict__ st,
                                          const zero_group_scalars* __restrict__ groups) {
-  const Entry en = entries[xcd_grouped(blockIdx.x, gridDim.x)];
+  constexpr int kParts = kUnits / U;
+  const int64_t b = xcd_grouped(blockIdx.x, gridDim.x);
+  const Entry en = entries[b / kParts];
   const Desc d = load_desc(descs, en.tensor);
   if (d.grad == nullptr) return;
-  const Share w = share_of(d, en.chunk);
+  const Share<U> w = share_of<U>(d, en.chunk, static_cast<int>(b % kParts));
   if (w.first >= d.numel) return;
-  if (w.first + kUnits * kBlock8 <= d.numel) {
-    adamw8_share<true>(d, w, host, seed, step, st, groups);
+  if (w.first + U * kBlock8 <= d.numel) {
+    adamw8_share<U, true>(d, w, host, seed, step, st, groups);
   } else {
-    adamw8_share<false>(d, w, host, seed, step, st, groups);
+    adamw8_share<U, false>(d, w, host, seed, step, st, groups);
   }
 }
 
@@ -877,37 +911,38 @@ __device__ __forceinline__ int64_t state32_at(const Desc& d, int64_t e) {
 }
 // A group of four elements never straddles two tiles of the fp32 state.
 // NULL parts read as zeros and are not written.
-template <bool FULL>
-__device__ __forceinline__ void load_part(const Desc& f, const Share& w, const float* part, f32x4 (&x)[kUnits]) {
+template <int U, bool FULL>
+__device__ __forceinline__ void load_part(const Desc& f, const Share<U>& w, const float* part, f32x4 (&x)[U]) {
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) x[u] = f32x4{0, 0, 0, 0};
+  for (int u = 0; u < U; ++u) x[u] = f32x4{0, 0, 0, 0};
   if (part == nullptr) return;
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) x[u] = load_have((gfloat)part + state32_at(f, w.elem(u)), w.have<FULL>(u));
+  for (int u = 0; u < U; ++u) x[u] = load_have((gfloat)part + state32_at(f, w.elem(u)), w.template have<FULL>(u));
 }
-template <bool FULL>
-__device__ __forceinline__ void store_part(const Desc& f, const Share& w, float* part, const f32x4 (&x)[kUnits]) {
+template <int U, bool FULL>
+__device__ __forceinline__ void store_part(const Desc& f, const Share<U>& w, float* part, const f32x4 (&x)[U]) {
   if (part == nullptr) return;
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) store_have((gfloat)part + state32_at(f, w.elem(u)), w.have<FULL>(u), x[u]);
+  for (int u = 0; u < U; ++u) store_have((gfloat)part + state32_at(f, w.elem(u)), w.template have<FULL>(u), x[u]);
 }
 
-template <bool FULL>
-__device__ __forceinline__ void pack_share(const Desc& f, const Share& w) {
-  f32x4 p[kUnits], m[kUnits], v[kUnits];
-  load_part<FULL>(f, w, f.m, m);
-  load_part<FULL>(f, w, f.v, v);
+template <int U, bool FULL>
+__device__ __forceinline__ void pack_share(const Desc& f, const Share<U>& w) {
+  f32x4 p[U], m[U], v[U];
+  load_part<U, FULL>(f, w, f.m, m);
+  load_part<U, FULL>(f, w, f.v, v);
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
+  for (int u = 0; u < U; ++u) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[u][k] = fabsf(v[u][k]);
   }
-  load_part<FULL>(f, w, f.state, p);
-  uint32_t mc[kUnits], vc[kUnits];
-  const float scale = encode_blocks(m, v, w.lane, [](int, int) { return u32x2{0x80000u, 0x80000u}; }, mc, vc);  // nearest
+  load_part<U, FULL>(f, w, f.state, p);
+  uint32_t mc[U], vc[U];
+  // half a step: nearest
+  const float scale = encode_blocks(m, v, w.lane, [](int, int) { return u32x2{0x80000u, 0x80000u}; }, mc, vc);
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int have = w.have<FULL>(u);
+  for (int u = 0; u < U; ++u) {
+    const int have = w.template have<FULL>(u);
     store_have(w.t.master + w.at(u), have, p[u]);
     store_codes(w.t.m + w.at(u), mc[u], have);
     store_codes(w.t.v + w.at(u), vc[u], have);
@@ -915,23 +950,24 @@ __device__ __forceinline__ void pack_share(const Desc& f, const Share& w) {
   w.store_scale(scale);
 }
 
-template <bool FULL>
-__device__ __forceinline__ void unpack_share(const Desc& f, const Share& w) {
-  f32x4 p[kUnits], m[kUnits], v[kUnits], sm, sv;
-  uint32_t mc[kUnits], vc[kUnits];
-  w.load_moments<FULL>(mc, vc, &sm, &sv);
+template <int U, bool FULL>
+__device__ __forceinline__ void unpack_share(const Desc& f, const Share<U>& w) {
+  f32x4 p[U], m[U], v[U];
+  float sm[U], sv[U];
+  uint32_t mc[U], vc[U];
+  w.template load_moments<FULL>(mc, vc, sm, sv);
   if (f.state != nullptr) {
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) p[u] = load_have(w.t.master + w.at(u), w.have<FULL>(u));
+    for (int u = 0; u < U; ++u) p[u] = load_have(w.t.master + w.at(u), w.template have<FULL>(u));
   }
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
+  for (int u = 0; u < U; ++u) {
     m[u] = decode_m(mc[u]) * sm[u];
     v[u] = decode_v(vc[u]) * sv[u];
   }
-  store_part<FULL>(f, w, f.m, m);
-  store_part<FULL>(f, w, f.v, v);
-  store_part<FULL>(f, w, f.state, p);
+  store_part<U, FULL>(f, w, f.m, m);
+  store_part<U, FULL>(f, w, f.v, v);
+  store_part<U, FULL>(f, w, f.state, p);
 }
 
 // Bound by HBM, 18 bytes an element either way: 195M parameters (tiled) pack in
@@ -942,13 +978,14 @@ STREAMING_KERNEL void list_state8_kernel(const Desc* __restrict__ descs32, const
                                          const Entry* __restrict__ entries8) {
   const Entry en = entries8[xcd_grouped(blockIdx.x, gridDim.x)];
   const Desc d = load_desc(descs8, en.tensor), f = load_desc(descs32, en.tensor);
-  const Share w = share_of(d, en.chunk);
+  constexpr int U = kUnits;
+  const Share<U> w = share_of<U>(d, en.chunk);
   if (w.first >= d.numel) return;
-  const bool full = w.first + kUnits * kBlock8 <= d.numel;
+  const bool full = w.first + U * kBlock8 <= d.numel;
   if constexpr (PACK) {
-    full ? pack_share<true>(f, w) : pack_share<false>(f, w);
+    full ? pack_share<U, true>(f, w) : pack_share<U, false>(f, w);
   } else {
-    full ? unpack_share<true>(f, w) : unpack_share<false>(f, w);
+    full ? unpack_share<U, true>(f, w) : unpack_share<U, false>(f, w);
   }
 }
 
@@ -1045,11 +1082,24 @@ int launch_list_adamw(const char* fn, const zero_list* l, const GroupTable& host
   });
 }
 
+// Up to one tile per compute unit, a block per wavefront instead of four: four
+// times the wavefronts, each with a quarter of the work.  Measured on MI355X:
+// 40,000 parameters in 16 ragged tensors 5.7 us on the GPU against 8.2; from
+// 512 whole tiles on the four-block form wins (7.4 against 8.6 us; 690 against
+// 749 us for 65,536).
+constexpr int64_t kFewTiles = 256;
 int launch_list_adamw8(const char* fn, const zero_list* l, const GroupTable& host, uint64_t seed, uint64_t step,
                        const zero_step_state* st, const zero_group_scalars* groups, void* stream) {
+  if (l->update_blocks == 0) return ZERO_OK;
+  if (l->update_blocks <= kFewTiles) {
+    hipLaunchKernelGGL(list_adamw8_kernel<1>, dim3(static_cast<unsigned>(kUnits * l->update_blocks)), dim3(kBlock), 0,
+                       static_cast<hipStream_t>(stream), descs_of(l), entries_of(l, l->update_offset), host, seed,
+                       step, st, groups);
+    return launch_status(fn);
+  }
   return for_each_list_launch(l, kTile8, fn, [&](const Entry* first, dim3 grid) {
-    hipLaunchKernelGGL(list_adamw8_kernel, grid, dim3(kBlock), 0, static_cast<hipStream_t>(stream), descs_of(l), first,
-                       host, seed, step, st, groups);
+    hipLaunchKernelGGL(list_adamw8_kernel<kUnits>, grid, dim3(kBlock), 0, static_cast<hipStream_t>(stream),
+                       descs_of(l), first, host, seed, step, st, groups);
   });
 }
 
@@ -1189,7 +1239,7 @@ int zero_list_adamw8_step(const zero_list* list, const zero_adamw_hparams* hp, u
   if (rc == ZERO_OK) rc = host_scalars(fn, list, hp, &host);
   if (rc != ZERO_OK) return rc;
   for (int32_t k = 0; k < list->n_groups; ++k) {
-    if (!(hp[k].eps >= 1e-16)) return fail(ZERO_ERR_INVALID, "%s: group %d: eps below 1e-16", fn, k);
+    if (!(static_cast<float>(hp[k].eps) >= kLeastEps8)) return fail(ZERO_ERR_INVALID, "%s: group %d: eps below 1e-16", fn, k);
     if (hp[k].step != hp[0].step) return fail(ZERO_ERR_INVALID, "%s: the groups' steps differ", fn);
   }
   return launch_list_adamw8(fn, list, host, seed, static_cast<uint64_t>(hp[0].step), nullptr, nullptr, stream);

@@ -6,7 +6,8 @@ flatten -> square-norm -> (simulated all-reduce + decision) -> AdamW.  Three
 ways of sequencing it: ``rank_step`` (decision on the host after a 16-byte
 readback), ``DeviceDecision`` (decision on the GPU, nothing waits on the
 host) and ``BucketPipeline`` (flatten + norm partials in constant-capacity
-buckets as gradients arrive on a producer stream).  No arithmetic of the
+buckets as gradients arrive on a producer stream).  ``TensorList`` and
+``ListDecision`` step many tensors where they lie.  No arithmetic of the
 method happens here: every step is a library call.
 """
 from __future__ import annotations
@@ -304,8 +305,10 @@ class TensorList:
     (``state`` tiled, or ``master``/``m``/``v``), 8-bit state (``state8``) or none (norm only).  Every argument is
     a list with one contiguous GPU tensor per list entry; ``grads`` and ``params`` may hold views at any element
     offset, and a gradient may be None (no gradient in this step: that tensor is left as it is).  Calls run on
-    the current stream of the tensors' device unless a stream is given; the table, the norm's workspace and the
-    tensors belong to the list, so calls that may overlap in time need lists of their own."""
+    the current stream of the tensors' device unless a stream is given.  The list keeps the tensors, its table and
+    the norm's workspace alive: keep it until its calls are done, and give calls that may overlap in time lists of
+    their own.  A captured graph replays what the table names at the time: `set_grads` between replays is seen, and
+    is itself not for capture."""
 
     def __init__(self, numels, grads=None, params=None, *, state=None, state8=None, master=None, m=None, v=None,
                  groups=None, n_groups: int = 1):
@@ -356,8 +359,13 @@ class TensorList:
         if bad:
             raise ValueError(f"gradients belong on {self.device} in bf16, fp16 or fp32, got {bad[0].dtype} on "
                              f"{bad[0].device}")
+        before = [t["grad"] for t in self._tensors]
         self._point(grads)
-        zero_list_repoint(self._tensors, self._host, self.list)
+        try:
+            zero_list_repoint(self._tensors, self._host, self.list)
+        except Exception:
+            self._point(before)  # the table still names them
+            raise
         n = self.list.grads_bytes
         if n:
             self.table[:n].copy_(torch.frombuffer(self._host, dtype=torch.uint8, count=n))
@@ -411,6 +419,7 @@ class ListDecision:
         if len(self.hparams) != tensors.list.n_groups:
             raise ValueError(f"{len(self.hparams)} configurations for {tensors.list.n_groups} groups")
         self.norms = torch.zeros(2, dtype=torch.float64, device=dev)  # square-norm, then its flag
+        self._sq, self._flag = self.norms.data_ptr(), self.norms.data_ptr() + 8
         self.state = torch.zeros(16, dtype=torch.float64, device=dev)
         self.groups = torch.zeros(12 * len(self.hparams), dtype=torch.float32, device=dev)
         with torch.cuda.device(dev):
@@ -418,10 +427,9 @@ class ListDecision:
 
     def step(self, stream=None) -> None:
         """Enqueues one whole step; nothing waits on the host."""
-        sq, flag = self.norms[:1], self.norms[1:].view(torch.int32)
-        self.tensors.grad_sqnorm(sq, flag, stream)
-        self.tensors._call(zero_list_decision_dev, sq, flag, 1, self.max_norm, self.hparams, self.state, self.groups,
-                           stream=stream)
+        self.tensors.grad_sqnorm(self._sq, self._flag, stream)
+        self.tensors._call(zero_list_decision_dev, self._sq, self._flag, 1, self.max_norm, self.hparams, self.state,
+                           self.groups, stream=stream)
         self.tensors.adamw_dev(self.state, self.groups, stream, self.seed)
 
     def read(self) -> dict:

@@ -470,6 +470,17 @@ def test_adamw8_special_blocks():
         assert_master8(new.master[at], p[at], st.master[at], m1, v1, s, f"block {k} master")
 
 
+def test_adamw8_least_eps():
+    """An eps of zero in the device form counts as 1e-16: where both moments are held as zeros nothing moves."""
+    n = 5000
+    x = List8([n], "fp32", "fp32", moments=[(np.zeros(n, np.float32), np.zeros(n, np.float32))], groups=1)
+    x.src.grads[0].zero_()
+    run = ListDecision(x.list, [AdamWConfig(eps=0.0, weight_decay=0.0)], max_norm=0.0)
+    run.step()
+    assert run.read()["skip"] == 0
+    assert_bits_equal(x.host(0).master, x.src.p[0], "master")
+
+
 def test_adamw8_rounding_depends_on_its_arguments_alone():
     def run(seed, step):
         x = List8([70001], seed=8, groups=1)
@@ -645,5 +656,6 @@ def test_tensor_list_refusals():
         lst.adamw(hparams(groups=2))
     with pytest.raises(Z.ZeroError):
         lst.set_grads([f])  # the master itself
+    assert lst._tensors[0]["grad"] is g  # what the table still names is kept alive
     with pytest.raises(ValueError, match="gradients"):
         lst.set_grads([g, g])
