@@ -103,9 +103,7 @@ def _counter_rows(d: str):
 def traffic_record(args) -> None:
     """Per-call HBM bytes of the tiled update from counter runs, each counter scaled by what it reads for a
     plain 1 GiB device copy (the runtime's copy kernel; the average is over the 1 GiB copies only, not the
-    runtime's small uploads through the same kernel).  Tied to the SHA-256 of the kernel source."""
-    import hashlib
-
+    runtime's small uploads through the same kernel).  Tied to the SHA-256 of the kernel source and its header."""
     import mixed_precision_adam_amd as Z
 
     w = workload(args)
@@ -126,12 +124,11 @@ def traffic_record(args) -> None:
     if not f or len(f) % lpc or len(wr) % lpc:
         raise SystemExit(f"{len(f)} / {len(wr)} update dispatches is not a whole number of {lpc}-launch calls")
     fk, wk = sum(f) / (len(f) // lpc), sum(wr) / (len(wr) // lpc)
-    src = os.path.join(ROOT, "mixed_precision_adam_amd", "csrc", "zero_shard.hip")
     rec = {"kernel": "adamw_tiled_kernel", "workload": w.name, "shard_numel": n, "launches_per_call": lpc,
            "calls_counted": len(f) // lpc, "fetch_kib_raw_per_call": fk, "write_kib_raw_per_call": wk,
            "fetch_scale": fs, "write_scale": ws, "bytes_per_call": (fk * fs + wk * ws) * 1024,
            "algorithmic_bytes": ADAM_BYTES_PER_PARAM * n,
-           "source_sha256": hashlib.sha256(open(src, "rb").read()).hexdigest(),
+           "source_sha256": _sha256("zero_shard.hip"), "header_sha256": _sha256("zero_common.h"),
            "source": "mixed_precision_adam_amd/csrc/zero_shard.hip",
            "summary": f"profiles/hbm_traffic_{w.name}.md"}
     out = os.path.join(ROOT, "profiles", f"traffic_adamw_tiled_kernel_{w.name}.json")
@@ -263,19 +260,26 @@ def copy_calibration(nbytes: int, reps: int = 10) -> None:
                       "flatten_copy_gbs": 2 * nbytes / sec_fl / 1e9}))
 
 
-def measured_traffic(kernel: str, workload: str):
-    """HBM bytes per update call of `kernel` (all of its launches) from the committed counter record, or None
-    when there is no record for this kernel and workload or the kernel source has changed since the
-    counters were taken."""
+def _sha256(source: str):
+    """Of a file under csrc/; None if it is not there."""
     import hashlib
 
+    path = os.path.join(ROOT, "mixed_precision_adam_amd", "csrc", source)
+    return hashlib.sha256(open(path, "rb").read()).hexdigest() if os.path.exists(path) else None
+
+
+def measured_traffic(kernel: str, workload: str):
+    """HBM bytes per update call of `kernel` (all of its launches) from the committed counter record, or None
+    when there is no record for this kernel and workload or the kernel source or its header has changed since
+    the counters were taken."""
     path = os.path.join(ROOT, "profiles", f"traffic_{kernel}_{workload}.json")
     if not os.path.exists(path):
         return None
     rec = json.load(open(path))
-    src = os.path.join(ROOT, "mixed_precision_adam_amd", "csrc", "zero_shard.hip")
-    sha = hashlib.sha256(open(src, "rb").read()).hexdigest()
-    if rec.get("source_sha256") != sha:
+    if rec.get("source_sha256") != _sha256("zero_shard.hip"):
+        return None
+    header = _sha256("zero_common.h")
+    if header is not None and rec.get("header_sha256") != header:
         return None
     return rec.get("bytes_per_call")
 
