@@ -405,8 +405,9 @@ constexpr uint32_t kInfBits = 0x7F800000u;
 // Workgroup b sums the squares of one chunk of one tensor's gradients.  Bound
 // by HBM reads: the 195M bf16 gradients of the GPT-2 rank's 47 pieces take
 // 62 us with the fold (6.3 TB/s), 60M fp32 ones in 500 ragged tensors 41 us.
-// Four vectors in flight per thread beat two by 13%; chunks of 8192 elements
-// are 15% slower, of 32,768 the same within the noise of 3%.
+// Four vectors in flight per thread beat two by 6% and eight by 5%, a cap of 4
+// wavefronts per SIMD 3 by 10% and 6 by 5%; chunks of 8192 elements are 15%
+// slower, of 32,768 the same within 3%.
 STREAMING_KERNEL void list_sqnorm_kernel(const Desc* __restrict__ descs, const Entry* __restrict__ entries,
                                          double* __restrict__ part_sum, uint32_t* __restrict__ part_bad) {
   double acc = 0.0;
@@ -514,6 +515,10 @@ constexpr float kSmallestPeak = 0x1p-110f;
 // A second moment whose block is held as zeros reads as 0: eps alone then
 // divides the first.
 constexpr float kLeastEps8 = 1e-16f;
+
+// Kernels with a cap of their own on the wavefronts per SIMD (STREAMING_KERNEL
+// has 4).
+#define WAVES_KERNEL(n) __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, n)))
 
 // A wavefront takes U adjacent blocks of a tile, lane l holding elements
 // 4l .. 4l+3 of each, so that every access of a wavefront is one contiguous
@@ -879,13 +884,15 @@ __device__ __forceinline__ void adamw8_share(const Desc& d, const Share<U>& w, c
 
 // Bound by HBM, 16 bytes an element (and 1/16 of scales) with 16-bit gradients
 // and parameters: the 842M parameters of the Llama-7B rank's pieces take
-// 2.15-2.20 ms (6.2-6.3 TB/s, where the fp32 update reaches 6.5-6.6 on the
+// 2.13-2.20 ms (6.2-6.4 TB/s, where the fp32 update reaches 6.5-6.6 on the
 // same box).  A block at a time per wavefront, with its own reductions and
 // divisions, took 3.3 ms: about 130 issue slots an element where HBM leaves
-// time for 98; now it is 50.  Caps of 3, 4 and 5 wavefronts per SIMD are
-// within 1%.
+// time for 98; now it is 50.  A cap of 3 wavefronts per SIMD (both timed in one
+// process) beats 4 and 5 by 1.1% there and by 2.1% on 60M ragged fp32 ones; 2
+// loses 2.6% and gains 0.5%.  XCD groups of 8 to 32 tiles are within 0.6%.
+// Without the non-temporal hint on the codes' loads or stores 9-13% slower.
 template <int U>
-STREAMING_KERNEL void list_adamw8_kernel(const Desc* __restrict__ descs, const Entry* __restrict__ entries,
+WAVES_KERNEL(3) void list_adamw8_kernel(const Desc* __restrict__ descs, const Entry* __restrict__ entries,
                                          GroupTable host, uint64_t seed, uint64_t step,
                                          const zero_step_state* __restrict__ st,
                                          const zero_group_scalars* __restrict__ groups) {
@@ -970,22 +977,34 @@ __device__ __forceinline__ void unpack_share(const Desc& f, const Share<U>& w) {
   store_part<U, FULL>(f, w, f.state, p);
 }
 
-// Bound by HBM, 18 bytes an element either way: 195M parameters (tiled) pack in
-// 560-570 us and unpack in 590-600 (6.2 and 5.9 TB/s; two thirds of the
-// unpack's bytes are written).
-template <bool PACK>
-STREAMING_KERNEL void list_state8_kernel(const Desc* __restrict__ descs32, const Desc* __restrict__ descs8,
+// Bound by HBM, 18 bytes an element either way, scales apart:
+// 195M parameters (tiled) pack in 533 us and unpack in 590 (6.6 and
+// 5.9 TB/s; two thirds of the unpack's bytes are written).  Pack with 2
+// wavefronts per SIMD beats 3 by 3.8% and 4 by 5.4%; unpack with 4 is within
+// 1% of 5 and 8 and 5% ahead of 3.
+WAVES_KERNEL(2) void list_pack8_kernel(const Desc* __restrict__ descs32, const Desc* __restrict__ descs8,
+                                       const Entry* __restrict__ entries8) {
+  const Entry en = entries8[xcd_grouped(blockIdx.x, gridDim.x)];
+  const Desc d = load_desc(descs8, en.tensor), f = load_desc(descs32, en.tensor);
+  const Share<kUnits> w = share_of<kUnits>(d, en.chunk);
+  if (w.first >= d.numel) return;
+  if (w.first + kUnits * kBlock8 <= d.numel) {
+    pack_share<kUnits, true>(f, w);
+  } else {
+    pack_share<kUnits, false>(f, w);
+  }
+}
+
+WAVES_KERNEL(4) void list_unpack8_kernel(const Desc* __restrict__ descs32, const Desc* __restrict__ descs8,
                                          const Entry* __restrict__ entries8) {
   const Entry en = entries8[xcd_grouped(blockIdx.x, gridDim.x)];
   const Desc d = load_desc(descs8, en.tensor), f = load_desc(descs32, en.tensor);
-  constexpr int U = kUnits;
-  const Share<U> w = share_of<U>(d, en.chunk);
+  const Share<kUnits> w = share_of<kUnits>(d, en.chunk);
   if (w.first >= d.numel) return;
-  const bool full = w.first + U * kBlock8 <= d.numel;
-  if constexpr (PACK) {
-    full ? pack_share<U, true>(f, w) : pack_share<U, false>(f, w);
+  if (w.first + kUnits * kBlock8 <= d.numel) {
+    unpack_share<kUnits, true>(f, w);
   } else {
-    full ? unpack_share<U, true>(f, w) : unpack_share<U, false>(f, w);
+    unpack_share<kUnits, false>(f, w);
   }
 }
 
@@ -1031,8 +1050,8 @@ const Entry* entries_of(const zero_list* l, int64_t offset) {
 }
 
 // Elements per launch with 8-bit state: about the bytes of the fp32 update's
-// 2^25 elements.  Measured on the Llama-7B rank's pieces: 2^25 2.25-2.27 ms,
-// 2^26 2.15-2.19, 2^27 2.14-2.21.
+// 2^25 elements.  Measured on the Llama-7B rank's pieces: 2^25 2.20 ms, 2^26
+// and 2^27 2.15.
 constexpr int64_t kElemsPerLaunch8 = int64_t(1) << 26;
 
 // Issues launch(first entry, count) for each launch over the list.
@@ -1112,12 +1131,8 @@ int convert(const char* fn, const zero_list* l32, const zero_list* l8, bool pack
   if (l32->n_tensors > 0 && (l32->state != 32 || l8->state != 8))
     return fail(ZERO_ERR_INVALID, "%s: needs a list with fp32 state and one with 8-bit state", fn);
   return for_each_list_launch(l8, kTile8, fn, [&](const Entry* first, dim3 grid) {
-    if (pack)
-      hipLaunchKernelGGL(list_state8_kernel<true>, grid, dim3(kBlock), 0, static_cast<hipStream_t>(stream),
-                         descs_of(l32), descs_of(l8), first);
-    else
-      hipLaunchKernelGGL(list_state8_kernel<false>, grid, dim3(kBlock), 0, static_cast<hipStream_t>(stream),
-                         descs_of(l32), descs_of(l8), first);
+    hipLaunchKernelGGL(pack ? list_pack8_kernel : list_unpack8_kernel, grid, dim3(kBlock), 0,
+                       static_cast<hipStream_t>(stream), descs_of(l32), descs_of(l8), first);
   });
 }
 

@@ -28,14 +28,15 @@ def asm(tmp_path_factory):
 def test_wide_accesses_are_nontemporal_and_global(asm):
     ks = test_codegen.kernels(asm)
     found = {k: [b for n, b in ks.items() if k in n] for k in ("list_sqnorm_kernel", "list_adamw_kernel",
-                                                                "list_adamw8_kernel", "list_state8_kernel")}
-    assert [len(v) for v in found.values()] == [1, 1, 2, 2]
+                                                                "list_adamw8_kernel", "list_pack8_kernel",
+                                                                "list_unpack8_kernel")}
+    assert [len(v) for v in found.values()] == [1, 1, 2, 1, 1]
     for kernel, bodies in found.items():
         for body in bodies:
             assert not [x for x in body if re.match(r"(flat|scratch)_", x)], kernel
             wide = [x for x in body if re.match(r"global_(load|store)_dwordx[24]\b", x)]
             plain = [x for x in wide if not re.search(r"\bnt\b", x)]
-            scales = 4 if kernel in ("list_adamw8_kernel", "list_state8_kernel") else 0  # m and v, whole and partial
+            scales = 4 if kernel in ("list_adamw8_kernel", "list_unpack8_kernel") else 0  # m and v, whole and partial
             others = 1 if kernel == "list_sqnorm_kernel" else 0  # the partial sum's store
             assert len(wide) >= 4 and len(plain) <= scales + others, f"{kernel}: {plain[:3]}"
 
