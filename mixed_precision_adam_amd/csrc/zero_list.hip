@@ -319,19 +319,25 @@ struct GroupTable {
   AdamScalars s[ZERO_LIST_MAX_GROUPS];
 };
 
+// From the device: every lane reads the same bytes and no kernel writes them
+// while this one runs, so they are constant memory here and come through the
+// scalar cache.
+template <typename T>
+__device__ __forceinline__ T uniform_load(const T* p) {
+  return *(const __attribute__((address_space(4))) T*)(uintptr_t)p;
+}
+
 __device__ __forceinline__ bool group_scalars(const GroupTable& host, const zero_step_state* st,
                                               const zero_group_scalars* groups, int group, AdamScalars* out) {
   if (st == nullptr) {
     *out = host.s[group];
     return true;
   }
-  // Every lane reads the same bytes and no kernel writes them while this one
-  // runs: constant memory, so they come through the scalar cache.
-  typedef const __attribute__((address_space(4))) int32_t* cint;
-  typedef const __attribute__((address_space(4))) float* cfloat;
-  if (*(cint)(uintptr_t)&st->skip) return false;
-  const cfloat s = (cfloat)(uintptr_t)groups[group].scalars;
-  *out = AdamScalars{s[0], s[1], s[2], s[3], s[4], s[5], s[6], s[7], s[8]};
+  if (uniform_load(&st->skip)) return false;
+  const float* s = groups[group].scalars;
+  *out = AdamScalars{uniform_load(s),     uniform_load(s + 1), uniform_load(s + 2),
+                     uniform_load(s + 3), uniform_load(s + 4), uniform_load(s + 5),
+                     uniform_load(s + 6), uniform_load(s + 7), uniform_load(s + 8)};
   return true;
 }
 
@@ -452,10 +458,12 @@ __global__ __launch_bounds__(kSmallThreads) void list_sqnorm_small_kernel(const 
 // distance of two chunks: 1024 floats (arrays) or a whole tile of
 // [master | m | v].  Bound by HBM, 28 bytes an element with 16-bit gradients
 // and parameters: the 195M parameters of the GPT-2 rank's pieces (tiled) take
-// 823 us (6.6 TB/s, the flat update's rate: the two table lookups ahead of the
-// data hide behind the other workgroups), 60M in 500 ragged tensors off the
-// 16-byte lines (arrays) 274 us (6.1 TB/s).  Without the cap at 4 wavefronts
-// per SIMD 847 and 282 us, at 3 831 and 284, at 5 836 and 276.
+// 823-829 us (6.6 TB/s, the flat update's rate: the two table lookups ahead of
+// the data hide behind the other workgroups), 60M in 500 ragged tensors off the
+// 16-byte lines (arrays) 274 us (6.1 TB/s).  Measured in one process on the
+// Llama-7B rank's 842M (tiled, 3.59 ms) and on the ragged ones: 3 wavefronts
+// per SIMD -0.5% and +1.7%, 5 +0.8% and +2.8%, 8 +2.1% and +4.2%; launches of
+// 2^24 elements +1.5% and +1.9%, of 2^26 +0.4% and -0.1%.
 STREAMING_KERNEL void list_adamw_kernel(const Desc* __restrict__ descs, const Entry* __restrict__ entries,
                                         GroupTable host, const zero_step_state* __restrict__ st,
                                         const zero_group_scalars* __restrict__ groups) {
@@ -520,11 +528,11 @@ constexpr float kLeastEps8 = 1e-16f;
 // has 4).
 #define WAVES_KERNEL(n) __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, n)))
 
-// A wavefront takes U adjacent blocks of a tile, lane l holding elements
-// 4l .. 4l+3 of each, so that every access of a wavefront is one contiguous
-// span.  With U = kUnits a 256-thread workgroup takes the tile.
-constexpr int kUnits = 4;
-static_assert(kTile8 == kUnits * kBlock8 * (kBlock / 64), "four wavefronts cover a tile");
+// A wavefront takes a block, lane l holding elements 4l .. 4l+3, so that every
+// access of a wavefront is one contiguous span and a block's peaks need no
+// shared memory; a tile's 16 blocks are four 256-thread workgroups.
+constexpr int kTileParts = static_cast<int>(kTile8Blocks / (kBlock / 64));
+static_assert(kBlock8 == 4 * 64, "a wavefront covers a block");
 
 // What four codes stand for, without their scale.  An m code is an OCP e4m3
 // number; a v code is the top of an fp32 pattern whose exponent lies 96 lower
@@ -564,95 +572,64 @@ __device__ __forceinline__ uint32_t signs(f32x4 m) {
   return (lo | hi) & 0x80808080u;
 }
 
-// max over lanes, one step: with lane l ^ the given distance of its row.
+// The larger of a lane's value and that of the lane of its row that CTRL names.
 template <int CTRL>
-__device__ __forceinline__ uint32_t max_dpp(uint32_t x, uint32_t y) {
-  const uint32_t z = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(y), CTRL, 0xF, 0xF, true));
-  return x > z ? x : z;
+__device__ __forceinline__ uint32_t max_dpp(uint32_t x) {
+  const uint32_t y = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, 0xF, 0xF, true));
+  return x > y ? x : y;
 }
 
-// The peaks of the wavefront's blocks, as bit patterns (so that a NaN
-// outweighs all): eight values at once, folding them onto each other while
-// the lanes are halved, in 4 + 2 + 1 + 3 steps where one value after the
-// other takes 8 x 6.  Group l / 8 of eight lanes ends with the peak of moment
-// (l / 32: m, v) of block peak_unit(l).
-// (One block: lanes 0 .. 31 and 32 .. 63 end with the peaks of m and v.)
-template <int U>
-__device__ __forceinline__ int peak_unit(int lane) {
-  return U == 1 ? 0 : ((lane >> 4) & 1) | ((lane >> 2) & 2);
-}
-__device__ __forceinline__ int peak_lane(int unit) { return ((unit & 1) << 4) | ((unit & 2) << 2); }
+// The peaks of a block, as bit patterns (so that a NaN outweighs all), from
+// those of its lanes: lanes 0 .. 31 end with m's and lanes 32 .. 63 with v's,
+// both moments in the same six steps.
 __device__ __forceinline__ uint32_t max_of(uint32_t a, uint32_t b) { return a > b ? a : b; }
-template <int U>
-__device__ __forceinline__ uint32_t fold_peaks(const uint32_t (&m)[U], const uint32_t (&v)[U], int lane) {
-  uint32_t r[U], x;
-#pragma unroll
-  for (int u = 0; u < U; ++u) {  // lanes 0 .. 31: m, 32 .. 63: v
-    const auto s = __builtin_amdgcn_permlane32_swap(m[u], v[u], false, false);
-    r[u] = max_of(s[0], s[1]);
-  }
-  if constexpr (U == 1) {
-    const auto s = __builtin_amdgcn_permlane16_swap(r[0], r[0], false, false);
-    x = max_of(s[0], s[1]);
-    x = max_dpp<0x128>(x, x);  // row_ror:8
-  } else {
-    uint32_t q[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {  // rows of 16: blocks 2u and 2u + 1 in turn
-      const auto s = __builtin_amdgcn_permlane16_swap(r[2 * u], r[2 * u + 1], false, false);
-      q[u] = max_of(s[0], s[1]);
-    }
-    const bool upper = (lane & 8) != 0;  // half rows: blocks 0, 1 and 2, 3
-    x = max_dpp<0x128>(upper ? q[1] : q[0], upper ? q[0] : q[1]);
-  }
-  x = max_dpp<0xB1>(x, x);      // quad_perm:[1,0,3,2]
-  x = max_dpp<0x4E>(x, x);      // quad_perm:[2,3,0,1]
-  return max_dpp<0x141>(x, x);  // row_half_mirror
+__device__ __forceinline__ uint32_t block_peaks(uint32_t m, uint32_t v) {
+  const auto halves = __builtin_amdgcn_permlane32_swap(m, v, false, false);
+  uint32_t x = max_of(halves[0], halves[1]);
+  const auto rows = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = max_of(rows[0], rows[1]);
+  x = max_dpp<0x128>(x);     // row_ror:8
+  x = max_dpp<0xB1>(x);      // quad_perm:[1,0,3,2]
+  x = max_dpp<0x4E>(x);      // quad_perm:[2,3,0,1]
+  return max_dpp<0x141>(x);  // row_half_mirror
 }
 
 __device__ __forceinline__ float read_lane(float x, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
 }
 
-// Codes of the wavefront's blocks (elements past the tensor's end are zeros
-// here), and this lane's scale: that of its group's block and moment.  One
-// division serves all eight.  dither(u, k): what element k of block u adds to
-// the positions of m and v.
-template <int U, typename F>
-__device__ __forceinline__ float encode_blocks(const f32x4 (&m)[U], const f32x4 (&v)[U], int lane, F&& dither,
-                                               uint32_t (&cm)[U], uint32_t (&cv)[U]) {
-  uint32_t pm[U], pv[U];
+// The codes of this lane's four elements (zeros past the tensor's end) and a
+// scale: m's in lanes 0 .. 31, v's in the others, so that one division serves
+// both.  dither(k): what element k adds to the positions of m and v.
+struct Codes {
+  uint32_t m, v;
+  float scale;
+};
+template <typename F>
+__device__ __forceinline__ Codes encode_block(f32x4 m, f32x4 v, int lane, F&& dither) {
+  float top_m = fabsf(m[0]);
+  uint32_t top_v = __float_as_uint(v[0]);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float a = fabsf(m[u][0]);
-    pv[u] = __float_as_uint(v[u][0]);
-#pragma unroll
-    for (int k = 1; k < 4; ++k) {
-      const uint32_t b = __float_as_uint(v[u][k]);
-      a = __builtin_elementwise_maximum(a, fabsf(m[u][k]));  // a NaN outweighs all here too
-      pv[u] = pv[u] > b ? pv[u] : b;
-    }
-    pm[u] = __float_as_uint(a);
+  for (int k = 1; k < 4; ++k) {
+    top_m = __builtin_elementwise_maximum(top_m, fabsf(m[k]));  // a NaN outweighs all here too
+    top_v = max_of(top_v, __float_as_uint(v[k]));
   }
-  const float peak = __uint_as_float(fold_peaks<U>(pm, pv, lane));
+  const float peak = __uint_as_float(block_peaks(__float_as_uint(top_m), top_v));
   const bool some = !(peak < kSmallestPeak);
-  const float scale = some ? peak * (lane < 32 ? 1.0f / kTopM : 1.0f / kTopV) : 0.0f;
+  Codes c;
+  c.scale = some ? peak * (lane < 32 ? 1.0f / kTopM : 1.0f / kTopV) : 0.0f;
   const float inv = some ? (lane < 32 ? kTopM : kTopV) / peak : 0.0f;
-  const uint64_t held = __ballot(some);
+  const float inv_m = read_lane(inv, 0), inv_v = read_lane(inv, 32);
+  const uint32_t least = static_cast<uint32_t>(__ballot(some) >> 32) & 1u;
+  c.m = signs(m);
+  c.v = 0;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const float inv_m = read_lane(inv, peak_lane(u)), inv_v = read_lane(inv, 32 + peak_lane(u));
-    const uint32_t least = static_cast<uint32_t>((held >> (32 + peak_lane(u))) & 1u);
-    cm[u] = signs(m[u]);
-    cv[u] = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const u32x2 add = dither(u, k);
-      cm[u] |= code_m(m[u][k], inv_m, add[0]) << (8 * k);
-      cv[u] |= code_v(v[u][k], inv_v, least, add[1]) << (8 * k);
-    }
+  for (int k = 0; k < 4; ++k) {
+    const u32x2 add = dither(k);
+    c.m |= code_m(m[k], inv_m, add[0]) << (8 * k);
+    c.v |= code_v(v[k], inv_v, least, add[1]) << (8 * k);
   }
-  return scale;
+  return c;
 }
 
 // The parts of one tile.
@@ -697,59 +674,37 @@ __device__ __forceinline__ void store_have(gfloat p, int have, f32x4 x) {
   for (int k = 0; k < have; ++k) p[k] = x[k];
 }
 
-// A wavefront's share of a tile.  FULL: all its elements are the tensor's.
-template <int U>
-struct Share {
-  static_assert(U == 1 || U == 4, "blocks of a wavefront");
-  int64_t first;  // its first element in the tensor
-  int64_t numel;
+// One block of a tensor and this lane's place in it.
+struct Block8 {
   Tile8 t;
-  int block, lane;  // its first block in the tile
-  __device__ int at(int u) const { return (block + u) * kBlock8 + 4 * lane; }  // in the tile
-  __device__ int64_t elem(int u) const { return first + u * kBlock8 + 4 * lane; }
+  int64_t first;  // the block's first element in the tensor
+  int64_t numel;
+  int block, lane;                                                  // the block's number in the tile
+  __device__ int at() const { return block * kBlock8 + 4 * lane; }  // in the tile
+  __device__ int64_t elem() const { return first + 4 * lane; }      // in the tensor
+  // How many of the lane's elements are the tensor's; FULL: all of the block's.
   template <bool FULL>
-  __device__ int have(int u) const {
+  __device__ int have() const {
     if (FULL) return 4;
-    const int64_t left = numel - elem(u);
+    const int64_t left = numel - elem();
     return left >= 4 ? 4 : left > 0 ? static_cast<int>(left) : 0;
-  }
-  template <bool FULL>
-  __device__ void load_moments(uint32_t (&mc)[U], uint32_t (&vc)[U], float (&sm)[U], float (&sv)[U]) const {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      mc[u] = load_codes(t.m + at(u), have<FULL>(u));
-      vc[u] = load_codes(t.v + at(u), have<FULL>(u));
-    }
-    if constexpr (U == 4) {
-      const f32x4 m4 = *(GLOBAL f32x4*)(t.scale_m + block), v4 = *(GLOBAL f32x4*)(t.scale_v + block);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        sm[u] = m4[u];
-        sv[u] = v4[u];
-      }
-    } else {
-      sm[0] = t.scale_m[block];
-      sv[0] = t.scale_v[block];
-    }
-  }
-  // The lane that holds a block's scale for all of its group writes it.
-  __device__ void store_scale(float scale) const {
-    const int u = peak_unit<U>(lane);
-    if ((lane & (U == 1 ? 31 : 7)) == 0 && first + u * kBlock8 < numel)
-      (lane < 32 ? t.scale_m : t.scale_v)[block + u] = scale;
   }
 };
 
-// `part`: which of the tile's kUnits / U workgroups this one is.
-template <int U>
-__device__ __forceinline__ Share<U> share_of(const Desc& d, uint32_t chunk, int part = 0) {
-  Share<U> s;
-  s.block = (part * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * U;
-  s.lane = threadIdx.x & 63;
-  s.first = static_cast<int64_t>(chunk) * kTile8 + s.block * kBlock8;
-  s.numel = d.numel;
-  s.t = tile8(d.state, chunk);
-  return s;
+// Block `block` of tile `chunk`, for the whole wavefront.
+__device__ __forceinline__ Block8 block_of(const Desc& d, uint32_t chunk, int block) {
+  Block8 b;
+  b.t = tile8(d.state, chunk);
+  b.block = __builtin_amdgcn_readfirstlane(block);
+  b.lane = threadIdx.x & 63;
+  b.first = static_cast<int64_t>(chunk) * kTile8 + b.block * kBlock8;
+  b.numel = d.numel;
+  return b;
+}
+
+// Lanes 0 and 32 hold the block's scales.
+__device__ __forceinline__ void store_scales(const Block8& w, float scale) {
+  if ((w.lane & 31) == 0) (w.lane < 32 ? w.t.scale_m : w.t.scale_v)[w.block] = scale;
 }
 
 // One element with the new moments in full precision: adam_element's moments,
@@ -757,8 +712,8 @@ __device__ __forceinline__ Share<U> share_of(const Desc& d, uint32_t chunk, int 
 // are the hardware's approximations (1 ulp each) and two products are fused
 // with their sums.  That changes the step p takes by at most 14·2^-24 of
 // itself, where the moments it is made of carry four bits, and the update runs
-// 4% faster than with correctly rounded ones (2.30 against 2.40 ms on the
-// Llama-7B rank's pieces).
+// 4% faster than with correctly rounded ones (2.30 against 2.40 ms with four
+// blocks a wavefront, 842M parameters).
 __device__ __forceinline__ void adam8_element(float g, float& p, float& m, float& v, const AdamScalars& s,
                                               float inv_bc2) {
   g = g * s.gscale;
@@ -774,139 +729,89 @@ __device__ __forceinline__ void adam8_element(float g, float& p, float& m, float
   p = __builtin_fmaf(p, s.decay, -u);
 }
 
-// The share's gradients as they lie, and as fp32; its parameters.  One branch
-// on the format each, so that the accesses are issued together.
-template <int U, int DT, bool FULL>
-__device__ __forceinline__ void load_grads(const Desc& d, const Share<U>& w, u32x4 (&g)[U]) {
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int have = w.template have<FULL>(u);
-    g[u] = u32x4{0, 0, 0, 0};
-    if (have == 4) {
-      g[u] = load_grad4(d.grad, DT, w.elem(u));
+// A lane's gradients as they lie (load_grad4's form).
+template <int DT>
+__device__ __forceinline__ u32x4 load_grads(const void* grad, int64_t e, int have) {
+  if (have == 4) return load_grad4(grad, DT, e);
+  u32x4 g = {0, 0, 0, 0};
+  for (int k = 0; k < have; ++k) {
+    if (DT == ZERO_FP32) {
+      g[k] = ((GLOBAL uint32_t*)grad)[e + k];
     } else {
-      for (int k = 0; k < have; ++k) {
-        if (DT == ZERO_FP32) {
-          g[u][k] = ((GLOBAL uint32_t*)d.grad)[w.elem(u) + k];
-        } else {
-          g[u][k >> 1] |= static_cast<uint32_t>(((gu16)d.grad)[w.elem(u) + k]) << (16 * (k & 1));
-        }
-      }
+      g[k >> 1] |= static_cast<uint32_t>(((gu16)grad)[e + k]) << (16 * (k & 1));
     }
   }
-}
-template <int U, int DT>
-__device__ __forceinline__ void widen_grads(const u32x4 (&raw)[U], f32x4 (&g)[U]) {
-#pragma unroll
-  for (int u = 0; u < U; ++u) g[u] = widen4(raw[u], DT);
-}
-template <int U, int DT, bool FULL>
-__device__ __forceinline__ void store_params(const Desc& d, const Share<U>& w, const f32x4 (&p)[U]) {
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int have = w.template have<FULL>(u);
-    if (have == 4) {
-      store_param4(d.param, DT, w.elem(u), p[u]);
-    } else {
-      for (int k = 0; k < have; ++k) store_param1(d.param, DT, w.elem(u) + k, p[u][k]);
-    }
-  }
+  return g;
 }
 
-template <int U, bool FULL>
-__device__ __forceinline__ void adamw8_share(const Desc& d, const Share<U>& w, const GroupTable& host, uint64_t seed,
+template <bool FULL>
+__device__ __forceinline__ void adamw8_block(const Desc& d, const Block8& w, const GroupTable& host, uint64_t seed,
                                              uint64_t step, const zero_step_state* st,
                                              const zero_group_scalars* groups) {
-  u32x4 g4[U];
-  f32x4 p[U], g[U], m[U], v[U];
-  float sm[U], sv[U];
-  uint32_t mc[U], vc[U];
-  if (d.gdt() == ZERO_FP32) {
-    load_grads<U, ZERO_FP32, FULL>(d, w, g4);
-  } else {
-    load_grads<U, ZERO_BF16, FULL>(d, w, g4);
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) p[u] = load_have(w.t.master + w.at(u), w.template have<FULL>(u));
-  w.template load_moments<FULL>(mc, vc, sm, sv);
+  const int have = w.have<FULL>(), at = w.at();
+  const u32x4 g4 = d.gdt() == ZERO_FP32 ? load_grads<ZERO_FP32>(d.grad, w.elem(), have)
+                                        : load_grads<ZERO_BF16>(d.grad, w.elem(), have);
+  f32x4 p = load_have(w.t.master + at, have);
+  const uint32_t mc = load_codes(w.t.m + at, have), vc = load_codes(w.t.v + at, have);
+  const float sm = w.t.scale_m[w.block], sv = w.t.scale_v[w.block];
   AdamScalars s;  // fetched while the data is on its way
   if (!group_scalars(host, st, groups, d.group(), &s)) return;
   s.eps = fmaxf(s.eps, kLeastEps8);
-  if (st != nullptr) step = static_cast<uint64_t>(st->adam_step);
-  const uint64_t base = mix64(seed + kGolden * step);
+  if (st != nullptr) step = static_cast<uint64_t>(uniform_load(&st->adam_step));
   const uint64_t block = static_cast<uint64_t>(d.block0 + w.first / kBlock8);
-  uint32_t key[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    key[u] = static_cast<uint32_t>(mix64(base + kGolden * (block + static_cast<uint64_t>(u) + 1)));
-  const uint32_t weyl = 4u * static_cast<uint32_t>(w.lane) * kWeyl;
+  const uint32_t key = static_cast<uint32_t>(mix64(mix64(seed + kGolden * step) + kGolden * (block + 1)));
+  const uint32_t r0 = key + 4u * static_cast<uint32_t>(w.lane) * kWeyl;
   const float inv_bc2 = __builtin_amdgcn_rcpf(s.bc2_sqrt);
-  if (d.gdt() == ZERO_BF16) {
-    widen_grads<U, ZERO_BF16>(g4, g);
-  } else if (d.gdt() == ZERO_FP16) {
-    widen_grads<U, ZERO_FP16>(g4, g);
-  } else {
-    widen_grads<U, ZERO_FP32>(g4, g);
-  }
+  const f32x4 g = widen4(g4, d.gdt());
+  f32x4 m = decode_m(mc) * sm, v = decode_v(vc) * sv;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int have = w.template have<FULL>(u);
-    m[u] = decode_m(mc[u]) * sm[u];
-    v[u] = decode_v(vc[u]) * sv[u];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float pk = p[u][k], mk = m[u][k], vk = v[u][k];
-      adam8_element(g[u][k], pk, mk, vk, s, inv_bc2);
-      p[u][k] = pk;
-      m[u][k] = FULL || k < have ? mk : 0.0f;
-      v[u][k] = FULL || k < have ? vk : 0.0f;
-    }
-    store_have(w.t.master + w.at(u), have, p[u]);
+  for (int k = 0; k < 4; ++k) {
+    float pk = p[k], mk = m[k], vk = v[k];
+    adam8_element(g[k], pk, mk, vk, s, inv_bc2);
+    p[k] = pk;
+    m[k] = FULL || k < have ? mk : 0.0f;
+    v[k] = FULL || k < have ? vk : 0.0f;
   }
-  if (d.pdt() == ZERO_BF16) {
-    store_params<U, ZERO_BF16, FULL>(d, w, p);
-  } else if (d.pdt() == ZERO_FP16) {
-    store_params<U, ZERO_FP16, FULL>(d, w, p);
+  store_have(w.t.master + at, have, p);
+  if (have == 4) {
+    store_param4(d.param, d.pdt(), w.elem(), p);
   } else {
-    store_params<U, ZERO_FP32, FULL>(d, w, p);
+    for (int k = 0; k < have; ++k) store_param1(d.param, d.pdt(), w.elem() + k, p[k]);
   }
-  const float scale = encode_blocks(m, v, w.lane, [&](int u, int k) {
-    const uint32_t r = key[u] + weyl + static_cast<uint32_t>(k) * kWeyl;
+  const Codes c = encode_block(m, v, w.lane, [&](int k) {
+    const uint32_t r = r0 + static_cast<uint32_t>(k) * kWeyl;
     return u32x2{r >> 12, r & 0xFFFFFu};
-  }, mc, vc);
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    store_codes(w.t.m + w.at(u), mc[u], w.template have<FULL>(u));
-    store_codes(w.t.v + w.at(u), vc[u], w.template have<FULL>(u));
-  }
-  w.store_scale(scale);
+  });
+  store_codes(w.t.m + at, c.m, have);
+  store_codes(w.t.v + at, c.v, have);
+  store_scales(w, c.scale);
 }
 
-// Bound by HBM, 16 bytes an element (and 1/16 of scales) with 16-bit gradients
-// and parameters: the 842M parameters of the Llama-7B rank's pieces take
-// 2.13-2.20 ms (6.2-6.4 TB/s, where the fp32 update reaches 6.5-6.6 on the
-// same box).  A block at a time per wavefront, with its own reductions and
-// divisions, took 3.3 ms: about 130 issue slots an element where HBM leaves
-// time for 98; now it is 50.  A cap of 3 wavefronts per SIMD (both timed in one
-// process) beats 4 and 5 by 1.1% there and by 2.1% on 60M ragged fp32 ones; 2
-// loses 2.6% and gains 0.5%.  XCD groups of 8 to 32 tiles are within 0.6%.
-// Without the non-temporal hint on the codes' loads or stores 9-13% slower.
-template <int U>
-WAVES_KERNEL(3) void list_adamw8_kernel(const Desc* __restrict__ descs, const Entry* __restrict__ entries,
-                                         GroupTable host, uint64_t seed, uint64_t step,
-                                         const zero_step_state* __restrict__ st,
-                                         const zero_group_scalars* __restrict__ groups) {
-  constexpr int kParts = kUnits / U;
+// Bound by HBM: 16 bytes an element (and 1/16 of scales) with 16-bit gradients
+// and parameters.  The 842M parameters of the Llama-7B rank's pieces take
+// 2.06-2.08 ms (6.5 TB/s, the fp32 update's rate), 60M ragged fp32 ones 188 us
+// (6.4 TB/s).  Measured in one process: 5, 6, 7 and 8 wavefronts per SIMD 2.11,
+// 2.08, 2.07 and 2.06 ms, and 186, 188, 190 and 192 us; four blocks a wavefront
+// (a quarter of the reductions and divisions, 104 registers) 2.13 ms and 197 us
+// at its best cap of 3; XCD groups of 8 to 96 workgroups within 1 and 2%.
+// Without the non-temporal hint on the codes 9-13% slower.  The instructions
+// have to be few: HBM leaves time for 98 issue slots an element, and a form
+// with separate reductions by shuffles, two divisions a block and correctly
+// rounded quotients took 130 of them and 3.3 ms.
+WAVES_KERNEL(6) void list_adamw8_kernel(const Desc* __restrict__ descs, const Entry* __restrict__ entries,
+                                        GroupTable host, uint64_t seed, uint64_t step,
+                                        const zero_step_state* __restrict__ st,
+                                        const zero_group_scalars* __restrict__ groups) {
   const int64_t b = xcd_grouped(blockIdx.x, gridDim.x);
-  const Entry en = entries[b / kParts];
+  const Entry en = entries[b / kTileParts];
   const Desc d = load_desc(descs, en.tensor);
   if (d.grad == nullptr) return;
-  const Share<U> w = share_of<U>(d, en.chunk, static_cast<int>(b % kParts));
+  const Block8 w = block_of(d, en.chunk, static_cast<int>(b % kTileParts) * (kBlock / 64) + (threadIdx.x >> 6));
   if (w.first >= d.numel) return;
-  if (w.first + U * kBlock8 <= d.numel) {
-    adamw8_share<U, true>(d, w, host, seed, step, st, groups);
+  if (w.first + kBlock8 <= d.numel) {
+    adamw8_block<true>(d, w, host, seed, step, st, groups);
   } else {
-    adamw8_share<U, false>(d, w, host, seed, step, st, groups);
+    adamw8_block<false>(d, w, host, seed, step, st, groups);
   }
 }
 
@@ -917,95 +822,101 @@ __device__ __forceinline__ int64_t state32_at(const Desc& d, int64_t e) {
   return d.layout() == ZERO_STATE_TILED ? e / kTile * (3 * kTile) + e % kTile : e;
 }
 // A group of four elements never straddles two tiles of the fp32 state.
-// NULL parts read as zeros and are not written.
-template <int U, bool FULL>
-__device__ __forceinline__ void load_part(const Desc& f, const Share<U>& w, const float* part, f32x4 (&x)[U]) {
-#pragma unroll
-  for (int u = 0; u < U; ++u) x[u] = f32x4{0, 0, 0, 0};
-  if (part == nullptr) return;
-#pragma unroll
-  for (int u = 0; u < U; ++u) x[u] = load_have((gfloat)part + state32_at(f, w.elem(u)), w.template have<FULL>(u));
-}
-template <int U, bool FULL>
-__device__ __forceinline__ void store_part(const Desc& f, const Share<U>& w, float* part, const f32x4 (&x)[U]) {
-  if (part == nullptr) return;
-#pragma unroll
-  for (int u = 0; u < U; ++u) store_have((gfloat)part + state32_at(f, w.elem(u)), w.template have<FULL>(u), x[u]);
-}
-
-template <int U, bool FULL>
-__device__ __forceinline__ void pack_share(const Desc& f, const Share<U>& w) {
-  f32x4 p[U], m[U], v[U];
-  load_part<U, FULL>(f, w, f.m, m);
-  load_part<U, FULL>(f, w, f.v, v);
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[u][k] = fabsf(v[u][k]);
-  }
-  load_part<U, FULL>(f, w, f.state, p);
-  uint32_t mc[U], vc[U];
+// A NULL part of the fp32 state reads as zeros.
+template <bool FULL>
+__device__ __forceinline__ void pack_block(const Desc& f, const Block8& w) {
+  const int have = w.have<FULL>(), at = w.at();
+  const int64_t at32 = state32_at(f, w.elem());
+  const f32x4 zero = {0, 0, 0, 0};
+  const f32x4 m = f.m ? load_have((gfloat)f.m + at32, have) : zero;
+  const f32x4 v = f.v ? load_have((gfloat)f.v + at32, have) : zero;
+  const f32x4 p = f.state ? load_have((gfloat)f.state + at32, have) : zero;
+  const f32x4 size_v = {fabsf(v[0]), fabsf(v[1]), fabsf(v[2]), fabsf(v[3])};
   // half a step: nearest
-  const float scale = encode_blocks(m, v, w.lane, [](int, int) { return u32x2{0x80000u, 0x80000u}; }, mc, vc);
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int have = w.template have<FULL>(u);
-    store_have(w.t.master + w.at(u), have, p[u]);
-    store_codes(w.t.m + w.at(u), mc[u], have);
-    store_codes(w.t.v + w.at(u), vc[u], have);
-  }
-  w.store_scale(scale);
+  const Codes c = encode_block(m, size_v, w.lane, [](int) { return u32x2{0x80000u, 0x80000u}; });
+  store_have(w.t.master + at, have, p);
+  store_codes(w.t.m + at, c.m, have);
+  store_codes(w.t.v + at, c.v, have);
+  store_scales(w, c.scale);
 }
 
+// U adjacent blocks, all loads ahead of the stores; a NULL part is not written.
 template <int U, bool FULL>
-__device__ __forceinline__ void unpack_share(const Desc& f, const Share<U>& w) {
-  f32x4 p[U], m[U], v[U];
-  float sm[U], sv[U];
+__device__ __forceinline__ void unpack_blocks(const Desc& f, const Block8 (&w)[U]) {
+  f32x4 p[U];
   uint32_t mc[U], vc[U];
-  w.template load_moments<FULL>(mc, vc, sm, sv);
-  if (f.state != nullptr) {
+  float sm[U], sv[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) p[u] = load_have(w.t.master + w.at(u), w.template have<FULL>(u));
+  for (int u = 0; u < U; ++u) {
+    mc[u] = load_codes(w[u].t.m + w[u].at(), w[u].template have<FULL>());
+    vc[u] = load_codes(w[u].t.v + w[u].at(), w[u].template have<FULL>());
+    sm[u] = w[u].t.scale_m[w[u].block];
+    sv[u] = w[u].t.scale_v[w[u].block];
+  }
+  if (f.state) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) p[u] = load_have(w[u].t.master + w[u].at(), w[u].template have<FULL>());
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    m[u] = decode_m(mc[u]) * sm[u];
-    v[u] = decode_v(vc[u]) * sv[u];
+    const int have = w[u].template have<FULL>();
+    const int64_t at32 = state32_at(f, w[u].elem());
+    if (f.m) store_have((gfloat)f.m + at32, have, decode_m(mc[u]) * sm[u]);
+    if (f.v) store_have((gfloat)f.v + at32, have, decode_v(vc[u]) * sv[u]);
+    if (f.state) store_have((gfloat)f.state + at32, have, p[u]);
   }
-  store_part<U, FULL>(f, w, f.m, m);
-  store_part<U, FULL>(f, w, f.v, v);
-  store_part<U, FULL>(f, w, f.state, p);
 }
 
-// Bound by HBM, 18 bytes an element either way, scales apart:
-// 195M parameters (tiled) pack in 533 us and unpack in 590 (6.6 and
-// 5.9 TB/s; two thirds of the unpack's bytes are written).  Pack with 2
-// wavefronts per SIMD beats 3 by 3.8% and 4 by 5.4%; unpack with 4 is within
-// 1% of 5 and 8 and 5% ahead of 3.
-WAVES_KERNEL(2) void list_pack8_kernel(const Desc* __restrict__ descs32, const Desc* __restrict__ descs8,
-                                       const Entry* __restrict__ entries8) {
-  const Entry en = entries8[xcd_grouped(blockIdx.x, gridDim.x)];
+// A wavefront of an unpacking workgroup: U adjacent blocks.
+template <int U>
+__device__ __forceinline__ void unpack_wave(const Desc* descs32, const Desc* descs8, const Entry* entries8) {
+  constexpr int kParts = kTileParts / U;  // workgroups per tile
+  const int64_t b = xcd_grouped(blockIdx.x, gridDim.x);
+  const Entry en = entries8[b / kParts];
   const Desc d = load_desc(descs8, en.tensor), f = load_desc(descs32, en.tensor);
-  const Share<kUnits> w = share_of<kUnits>(d, en.chunk);
-  if (w.first >= d.numel) return;
-  if (w.first + kUnits * kBlock8 <= d.numel) {
-    pack_share<kUnits, true>(f, w);
+  Block8 w[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    w[u] = block_of(d, en.chunk, (static_cast<int>(b % kParts) * (kBlock / 64) + (threadIdx.x >> 6)) * U + u);
+  if (w[0].first >= d.numel) return;
+  if (w[U - 1].first + kBlock8 <= d.numel) {
+    unpack_blocks<U, true>(f, w);
   } else {
-    pack_share<kUnits, false>(f, w);
+    unpack_blocks<U, false>(f, w);
   }
 }
 
-WAVES_KERNEL(4) void list_unpack8_kernel(const Desc* __restrict__ descs32, const Desc* __restrict__ descs8,
+// Bound by HBM, 18 bytes an element either way, scales apart.  What differs is
+// how many bytes in flight suit each mix of reads and writes (measured on
+// MI355X in one process; the GPT-2 rank's 195M parameters, tiled, the
+// Llama-7B rank's 842M, 60M in ragged arrays):
+//   pack: one block a wavefront, 4 wavefronts per SIMD 518-521 us (6.7 TB/s)
+//     for 195M, 3 556, 6 522, 8 531; four blocks at 2 531, at 4 563;
+//   unpack of master and moments: one block, 3 per SIMD 545 us (6.4 TB/s) for
+//     195M and 174 us for 60M, 4 576 and 172; four blocks at 4 595 and 186;
+//   unpack of moments alone: four blocks, 2 per SIMD 1.36 ms (6.2 TB/s) for
+//     842M and 95 us for 60M, at 4 1.47 and 108; one block at 3 and 4
+//     1.83-2.18 and 124-147, at 8 1.47 and 104.
+STREAMING_KERNEL void list_pack8_kernel(const Desc* __restrict__ descs32, const Desc* __restrict__ descs8,
+                                        const Entry* __restrict__ entries8) {
+  const int64_t b = xcd_grouped(blockIdx.x, gridDim.x);
+  const Entry en = entries8[b / kTileParts];
+  const Desc d = load_desc(descs8, en.tensor), f = load_desc(descs32, en.tensor);
+  const Block8 w = block_of(d, en.chunk, static_cast<int>(b % kTileParts) * (kBlock / 64) + (threadIdx.x >> 6));
+  if (w.first >= d.numel) return;
+  if (w.first + kBlock8 <= d.numel) {
+    pack_block<true>(f, w);
+  } else {
+    pack_block<false>(f, w);
+  }
+}
+WAVES_KERNEL(3) void list_unpack8_kernel(const Desc* __restrict__ descs32, const Desc* __restrict__ descs8,
                                          const Entry* __restrict__ entries8) {
-  const Entry en = entries8[xcd_grouped(blockIdx.x, gridDim.x)];
-  const Desc d = load_desc(descs8, en.tensor), f = load_desc(descs32, en.tensor);
-  const Share<kUnits> w = share_of<kUnits>(d, en.chunk);
-  if (w.first >= d.numel) return;
-  if (w.first + kUnits * kBlock8 <= d.numel) {
-    unpack_share<kUnits, true>(f, w);
-  } else {
-    unpack_share<kUnits, false>(f, w);
-  }
+  unpack_wave<1>(descs32, descs8, entries8);
+}
+WAVES_KERNEL(2) void list_unpack8_moments_kernel(const Desc* __restrict__ descs32, const Desc* __restrict__ descs8,
+                                                 const Entry* __restrict__ entries8) {
+  unpack_wave<4>(descs32, descs8, entries8);
 }
 
 // ------------------------------------------------------------------ decision
@@ -1050,8 +961,8 @@ const Entry* entries_of(const zero_list* l, int64_t offset) {
 }
 
 // Elements per launch with 8-bit state: about the bytes of the fp32 update's
-// 2^25 elements.  Measured on the Llama-7B rank's pieces: 2^25 2.20 ms, 2^26
-// and 2^27 2.15.
+// 2^25 elements.  Measured in one process: 842M parameters 2.09 ms with 2^25,
+// 2.08 with 2^26, 2.07 with 2^27; 60M 194, 188 and 188 us.
 constexpr int64_t kElemsPerLaunch8 = int64_t(1) << 26;
 
 // Issues launch(first entry, count) for each launch over the list.
@@ -1101,24 +1012,12 @@ int launch_list_adamw(const char* fn, const zero_list* l, const GroupTable& host
   });
 }
 
-// Up to one tile per compute unit, a block per wavefront instead of four: four
-// times the wavefronts, each with a quarter of the work.  Measured on MI355X:
-// 40,000 parameters in 16 ragged tensors 5.7 us on the GPU against 8.2; from
-// 512 whole tiles on the four-block form wins (7.4 against 8.6 us; 690 against
-// 749 us for 65,536).
-constexpr int64_t kFewTiles = 256;
 int launch_list_adamw8(const char* fn, const zero_list* l, const GroupTable& host, uint64_t seed, uint64_t step,
                        const zero_step_state* st, const zero_group_scalars* groups, void* stream) {
-  if (l->update_blocks == 0) return ZERO_OK;
-  if (l->update_blocks <= kFewTiles) {
-    hipLaunchKernelGGL(list_adamw8_kernel<1>, dim3(static_cast<unsigned>(kUnits * l->update_blocks)), dim3(kBlock), 0,
-                       static_cast<hipStream_t>(stream), descs_of(l), entries_of(l, l->update_offset), host, seed,
-                       step, st, groups);
-    return launch_status(fn);
-  }
   return for_each_list_launch(l, kTile8, fn, [&](const Entry* first, dim3 grid) {
-    hipLaunchKernelGGL(list_adamw8_kernel<kUnits>, grid, dim3(kBlock), 0, static_cast<hipStream_t>(stream),
-                       descs_of(l), first, host, seed, step, st, groups);
+    grid.x *= kTileParts;
+    hipLaunchKernelGGL(list_adamw8_kernel, grid, dim3(kBlock), 0, static_cast<hipStream_t>(stream), descs_of(l), first,
+                       host, seed, step, st, groups);
   });
 }
 
@@ -1130,9 +1029,13 @@ int convert(const char* fn, const zero_list* l32, const zero_list* l8, bool pack
     return fail(ZERO_ERR_INVALID, "%s: the two lists' tensors differ in size", fn);
   if (l32->n_tensors > 0 && (l32->state != 32 || l8->state != 8))
     return fail(ZERO_ERR_INVALID, "%s: needs a list with fp32 state and one with 8-bit state", fn);
+  const bool whole = (l32->flags & ZERO_LIST_WHOLE_STATE) != 0;
+  const auto kernel = pack ? list_pack8_kernel : whole ? list_unpack8_kernel : list_unpack8_moments_kernel;
+  const unsigned parts = pack || whole ? kTileParts : kTileParts / 4;  // workgroups per tile
   return for_each_list_launch(l8, kTile8, fn, [&](const Entry* first, dim3 grid) {
-    hipLaunchKernelGGL(pack ? list_pack8_kernel : list_unpack8_kernel, grid, dim3(kBlock), 0,
-                       static_cast<hipStream_t>(stream), descs_of(l32), descs_of(l8), first);
+    grid.x *= parts;
+    hipLaunchKernelGGL(kernel, grid, dim3(kBlock), 0, static_cast<hipStream_t>(stream), descs_of(l32), descs_of(l8),
+                       first);
   });
 }
 
@@ -1254,7 +1157,8 @@ int zero_list_adamw8_step(const zero_list* list, const zero_adamw_hparams* hp, u
   if (rc == ZERO_OK) rc = host_scalars(fn, list, hp, &host);
   if (rc != ZERO_OK) return rc;
   for (int32_t k = 0; k < list->n_groups; ++k) {
-    if (!(static_cast<float>(hp[k].eps) >= kLeastEps8)) return fail(ZERO_ERR_INVALID, "%s: group %d: eps below 1e-16", fn, k);
+    if (!(static_cast<float>(hp[k].eps) >= kLeastEps8))
+      return fail(ZERO_ERR_INVALID, "%s: group %d: eps below 1e-16", fn, k);
     if (hp[k].step != hp[0].step) return fail(ZERO_ERR_INVALID, "%s: the groups' steps differ", fn);
   }
   return launch_list_adamw8(fn, list, host, seed, static_cast<uint64_t>(hp[0].step), nullptr, nullptr, stream);
