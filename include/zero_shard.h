@@ -507,7 +507,8 @@ int64_t zero_list_table_bytes(const zero_list_tensor* tensors, int32_t n_tensors
  *   With ZERO_STATE_ARRAYS any of state, m and v may be NULL: such a list can
  * only be the source or target of a conversion (a NULL target part is not
  * written, a NULL source part reads as zeros).  Tensors of no elements are
- * valid and are passed over. */
+ * valid and are passed over.  A list holds at most 2^23 chunks of 16,384
+ * elements, counted by tensor. */
 int zero_list_plan(const zero_list_tensor* tensors, int32_t n_tensors, int32_t n_groups, void* table_host,
                    int64_t table_bytes, zero_list* out);
 
@@ -552,7 +553,8 @@ typedef struct zero_group_scalars {
  * *state_dev (whose own scalars become group 0's), and, unless the step is
  * skipped, the scalars of every group into groups_dev[n_groups] (16-byte
  * aligned).  hp[n_groups] on the host: lr, beta1, beta2, eps and weight_decay
- * are used.  n_groups in [1, ZERO_LIST_MAX_GROUPS]. */
+ * are used, and are fixed in a captured graph.  n_groups in
+ * [1, ZERO_LIST_MAX_GROUPS]. */
 int zero_list_decision_dev(const double* rank_sqnorms_dev, const int32_t* rank_flags_dev, int32_t n_ranks,
                            double max_norm, const zero_adamw_hparams* hp, int32_t n_groups,
                            zero_step_state* state_dev, zero_group_scalars* groups_dev, void* stream);

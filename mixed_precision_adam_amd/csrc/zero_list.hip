@@ -32,7 +32,7 @@ struct Desc {
   float* m;
   float* v;
   int64_t numel;
-  int64_t block0;  // number of the tensor's first block of ZERO_STATE8_BLOCK elements in the list
+  int64_t block0;    // number of the tensor's first block of ZERO_STATE8_BLOCK elements in the list
   uint32_t formats;  // gradient, parameter, layout, group: one byte each
   uint32_t reserved;
   __host__ __device__ int gdt() const { return static_cast<int>(formats & 0xFFu); }
@@ -410,7 +410,8 @@ constexpr uint32_t kInfBits = 0x7F800000u;
 
 // Workgroup b sums the squares of one chunk of one tensor's gradients.  Bound
 // by HBM reads: the 195M bf16 gradients of the GPT-2 rank's 47 pieces take
-// 62 us with the fold (6.3 TB/s), 60M fp32 ones in 500 ragged tensors 41 us.
+// 58-62 us with the fold (6.3-6.7 TB/s), 60M fp32 ones in 500 ragged tensors
+// 38-41 us; the fold, a launch of its own, is 4.5-5 us of either.
 // Four vectors in flight per thread beat two by 6% and eight by 5%, a cap of 4
 // wavefronts per SIMD 3 by 10% and 6 by 5%; chunks of 8192 elements are 15%
 // slower, of 32,768 the same within 3%.
@@ -821,8 +822,9 @@ WAVES_KERNEL(6) void list_adamw8_kernel(const Desc* __restrict__ descs, const En
 __device__ __forceinline__ int64_t state32_at(const Desc& d, int64_t e) {
   return d.layout() == ZERO_STATE_TILED ? e / kTile * (3 * kTile) + e % kTile : e;
 }
-// A group of four elements never straddles two tiles of the fp32 state.
-// A NULL part of the fp32 state reads as zeros.
+
+// A lane's four elements never straddle two tiles of the fp32 state, whose
+// NULL parts read as zeros.
 template <bool FULL>
 __device__ __forceinline__ void pack_block(const Desc& f, const Block8& w) {
   const int have = w.have<FULL>(), at = w.at();
@@ -900,6 +902,7 @@ __device__ __forceinline__ void unpack_wave(const Desc* descs32, const Desc* des
 //     compute unit) take the one-block form here too: 40,000 elements 3.2 us
 //     on the GPU against 4.6.
 constexpr int64_t kFewTiles = 256;
+
 STREAMING_KERNEL void list_pack8_kernel(const Desc* __restrict__ descs32, const Desc* __restrict__ descs8,
                                         const Entry* __restrict__ entries8) {
   const int64_t b = xcd_grouped(blockIdx.x, gridDim.x);
@@ -913,10 +916,12 @@ STREAMING_KERNEL void list_pack8_kernel(const Desc* __restrict__ descs32, const 
     pack_block<false>(f, w);
   }
 }
+
 WAVES_KERNEL(3) void list_unpack8_kernel(const Desc* __restrict__ descs32, const Desc* __restrict__ descs8,
                                          const Entry* __restrict__ entries8) {
   unpack_wave<1>(descs32, descs8, entries8);
 }
+
 WAVES_KERNEL(2) void list_unpack8_moments_kernel(const Desc* __restrict__ descs32, const Desc* __restrict__ descs8,
                                                  const Entry* __restrict__ entries8) {
   unpack_wave<4>(descs32, descs8, entries8);

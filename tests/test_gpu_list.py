@@ -240,6 +240,66 @@ def test_adamw_over_many_tensors():
     x.check()
 
 
+def test_adamw_mixed_list():
+    """Every tensor with formats, layout, group and alignment of its own, in one list."""
+    rng = np.random.default_rng(12)
+    guard, tensors, parts = Guarded(), [], []
+    kinds = [(g, p, lay) for g in FLOATS for p in FLOATS for lay in ("arrays", "tiled")]
+    for k, (grad, param, layout) in enumerate(kinds):
+        x = List32([700 + 301 * k], grad, param, layout, k % 4, seed=40 + k, groups=1)
+        x.group = [int(rng.integers(0, 2))]
+        held = {f: v[0] for f, v in x.held.items()}
+        held["state"] = held.pop("master", held.get("state"))
+        code = {torch.bfloat16: Z.ZERO_BF16, torch.float16: Z.ZERO_FP16, torch.float32: Z.ZERO_FP32}
+        tensors.append(dict(numel=x.sizes[0], grad=x.grads[0], param=x.param[0], gdt=code[FLOATS[grad]],
+                            pdt=code[FLOATS[param]], group=x.group[0],
+                            layout=Z.ZERO_STATE_TILED if layout == "tiled" else Z.ZERO_STATE_ARRAYS, **held))
+        parts.append(x)
+    lst, table = Z.zero_list_plan(tensors, 2)
+    table_dev = torch.frombuffer(table, dtype=torch.uint8).to(DEV)
+    lst.table_dev = table_dev.data_ptr()
+    Z.zero_list_adamw_step(lst, hparams(4))
+    ws = torch.empty(Z.zero_list_grad_sqnorm_workspace_bytes(lst), dtype=torch.uint8, device=DEV)
+    out = guard(torch.zeros(1, dtype=torch.float64))
+    flag = guard(torch.zeros(1, dtype=torch.int32))
+    Z.zero_list_grad_sqnorm(lst, ws, ws.numel(), out, flag)
+    want = math.fsum(float(v) ** 2 for x in parts for v in x.g[0].float())
+    assert abs(float(out[0]) - want) <= lst.numel * 2.0**-53 * want and int(flag[0]) == 0
+    for k, x in enumerate(parts):
+        x.plain_step(4, 1.0)
+        x.check(f"{kinds[k]}")
+    guard.check()
+
+
+@pytest.mark.parametrize("param", ["bf16", "fp16"])
+@pytest.mark.parametrize("eight", [False, True])
+def test_parameter_rounding(param, eight):
+    """Masters on and beside every rounding boundary of the format, zeros, subnormals, infinities and NaN, left as they
+    are by a learning rate of zero: each parameter is the master's nearest value, ties to even."""
+    if param == "fp16":
+        p = parity.f16_probe_bits(20_000).view(np.float32)
+    else:
+        b = np.arange(1 << 16, dtype=np.uint32) << 16
+        p = np.concatenate([b, b + 0x7FFF, b + 0x8000, b + 0x8001, b + 1]).view(np.float32)
+    n = len(p)
+    zero = np.zeros(n, np.float32)
+    hp = Z.zero_list_hparams([dict(CFG[0], lr=0.0)])
+    x = (List8 if eight else List32)([n], "bf16", param, **({} if eight else dict(layout="tiled", shift=0)), seed=0,
+                                     groups=1)
+    src = x.src if eight else x
+    st = torch.from_numpy(p).to(DEV)
+    if eight:
+        TensorList([n], master=[st], m=[torch.from_numpy(zero).to(DEV)], v=[torch.from_numpy(zero).to(DEV)]).pack8(
+            x.list)
+    else:
+        Z.zero_state_tile(st, *[torch.from_numpy(zero).to(DEV)] * 2, x.held["state"][0], n)
+    x.list.adamw(hp)
+    # (p·decay - step turns -0 into +0 where the step is -0, as the formula does: the master says which)
+    master = x.host(0).master.copy() if eight else x.state(0)[0]
+    assert np.array_equal(master, p, equal_nan=True)
+    assert_bits_equal(param_bits(src.param[0]), param_bits(torch.from_numpy(master).to(FLOATS[param])), param)
+
+
 @pytest.mark.parametrize("layout", ["arrays", "tiled"])
 def test_adamw_extreme_values(layout):
     """Infinities, NaN, subnormals and the largest numbers do what the plain form does."""
@@ -331,8 +391,8 @@ def test_pack_and_unpack(layout, shift):
 
 
 @pytest.mark.parametrize("missing", ["master", "m", "v"])
-def test_conversion_passes_over_missing_parts(missing):
-    n = 5001
+@pytest.mark.parametrize("n", [5001, 1_300_003])  # within one tile per compute unit, and past it
+def test_conversion_passes_over_missing_parts(missing, n):
     src = List32([n], "bf16", "bf16", "arrays", 0, seed=1, groups=1)
     state = torch.zeros(Z.zero_state8_bytes(n), dtype=torch.uint8, device=DEV)
     lst = TensorList([n], state8=[state])
