@@ -443,7 +443,9 @@ def zero_list_hparams(groups):
 
 def _list_tensors(tensors):
     """Dicts with the fields of zero_list_tensor -> a C array, every tensor's size checked against what the call
-    will touch."""
+    will touch.  An array is taken as it is."""
+    if isinstance(tensors, C.Array):
+        return tensors
     out = (zero_list_tensor * max(len(tensors), 1))()
     for t, rec in zip(tensors, out):
         n, layout = int(t["numel"]), t.get("layout", ZERO_STATE_NONE)
@@ -463,7 +465,8 @@ def zero_list_table_bytes(tensors) -> int:
 
 
 def zero_list_plan(tensors, n_groups: int = 1):
-    """(zero_list, table as a bytearray).  The caller copies the table to the device and sets table_dev."""
+    """(zero_list, table as a bytearray) of a list of dicts or an array of zero_list_tensor.  The caller copies the
+    table to the device and sets table_dev."""
     recs, out = _list_tensors(tensors), zero_list()
     size = _lib.zero_list_table_bytes(C.cast(recs, _P), len(tensors))
     if size == 0:

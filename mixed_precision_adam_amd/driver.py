@@ -18,14 +18,14 @@ import numpy as np
 import torch
 
 from . import (ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO_STATE_8BIT, ZERO_STATE_ARRAYS, ZERO_STATE_NONE, ZERO_STATE_TILE,
-               ZERO_STATE_TILED, read_step_state, zero_adamw_step, zero_adamw_step_dev,
-               zero_adamw_step_tiled, zero_adamw_step_tiled_dev, zero_bucket_segments, zero_flatten_grads,
-               zero_flatten_grads_partials, zero_flatten_grads_sqnorm, zero_flatten_partials_count,
-               zero_flatten_plan, zero_grad_sqnorm, zero_grad_sqnorm_workspace_bytes, zero_list_adamw8_step,
-               zero_list_adamw8_step_dev, zero_list_adamw_step, zero_list_adamw_step_dev, zero_list_decision_dev,
-               zero_list_grad_sqnorm, zero_list_grad_sqnorm_workspace_bytes, zero_list_hparams, zero_list_plan,
-               zero_list_repoint, zero_list_state8_pack, zero_list_state8_unpack, zero_shard_layout,
-               zero_sqnorm_reduce, zero_state_tile, zero_state_tiled_numel, zero_state_untile, zero_step_decision,
+               ZERO_STATE_TILED, _buf, read_step_state, zero_adamw_step, zero_adamw_step_dev, zero_adamw_step_tiled,
+               zero_adamw_step_tiled_dev, zero_bucket_segments, zero_flatten_grads, zero_flatten_grads_partials,
+               zero_flatten_grads_sqnorm, zero_flatten_partials_count, zero_flatten_plan, zero_grad_sqnorm,
+               zero_grad_sqnorm_workspace_bytes, zero_list_adamw8_step, zero_list_adamw8_step_dev,
+               zero_list_adamw_step, zero_list_adamw_step_dev, zero_list_decision_dev, zero_list_grad_sqnorm,
+               zero_list_grad_sqnorm_workspace_bytes, zero_list_hparams, zero_list_plan, zero_list_repoint,
+               zero_list_state8_pack, zero_list_state8_unpack, zero_list_tensor, zero_shard_layout, zero_sqnorm_reduce,
+               zero_state8_bytes, zero_state_tile, zero_state_tiled_numel, zero_state_untile, zero_step_decision,
                zero_step_decision_dev, zero_step_state_init)
 
 _FORMAT = {torch.bfloat16: ZERO_BF16, torch.float16: ZERO_FP16, torch.float32: ZERO_FP32}
@@ -330,14 +330,20 @@ class TensorList:
                   ZERO_STATE_ARRAYS if any(x is not None for x in (master, m, v)) else ZERO_STATE_NONE)
         self.device = devices.pop() if devices else torch.device("cuda", torch.cuda.current_device())
         state = next((x for x in (state, state8, master) if x is not None), None)
-        self._tensors = [dict(numel=n, layout=layout, group=groups[k] if groups is not None else 0,
-                              **{f: x[k] for f, x in (("param", params), ("state", state), ("m", m), ("v", v))
-                                 if x is not None}) for k, n in enumerate(numels)]
-        for t in self._tensors:
-            if t.get("param") is not None:
-                t["pdt"] = _FORMAT[t["param"].dtype]
-        self._point(grads)
-        self.list, self._host = zero_list_plan(self._tensors, n_groups)
+        self._kept = (params, state, m, v)  # the table names them
+        self._grads = list(grads) if grads is not None else [None] * len(numels)
+        self._recs = (zero_list_tensor * len(numels))()
+        for k, rec in enumerate(self._recs):
+            n = max(int(numels[k]), 0)
+            rec.numel, rec.layout, rec.group = int(numels[k]), layout, groups[k] if groups is not None else 0
+            size = {ZERO_STATE_TILED: 4 * zero_state_tiled_numel(n), ZERO_STATE_8BIT: zero_state8_bytes(n)}
+            if params is not None and params[k] is not None:
+                rec.param, rec.pdt = _buf(params[k], n * params[k].element_size()), _FORMAT[params[k].dtype]
+            rec.state = _buf(state[k], size.get(layout, 4 * n)) if state is not None else None
+            rec.m = _buf(m[k], 4 * n) if m is not None else None
+            rec.v = _buf(v[k], 4 * n) if v is not None else None
+        self._point(self._grads)
+        self.list, self._host = zero_list_plan(self._recs, n_groups)
         self.table = torch.frombuffer(self._host, dtype=torch.uint8).to(self.device)
         self.list.table_dev = self.table.data_ptr()
         self.ws_bytes = zero_list_grad_sqnorm_workspace_bytes(self.list)
@@ -345,27 +351,27 @@ class TensorList:
         self.state8 = state8 is not None
 
     def _point(self, grads) -> None:
-        for k, t in enumerate(self._tensors):
-            t["grad"] = None if grads is None else grads[k]
-            if t["grad"] is not None:
-                t["gdt"] = _FORMAT[t["grad"].dtype]
+        found = [(None, ZERO_BF16) if g is None else (_buf(g, max(rec.numel, 0) * g.element_size()), _FORMAT[g.dtype])
+                 for g, rec in zip(grads, self._recs)]  # all of them checked before any is taken
+        for rec, (address, dtype) in zip(self._recs, found):
+            rec.grad, rec.gdt = address, dtype
 
     def set_grads(self, grads) -> None:
         """Other gradient tensors (or None) for the coming steps: rewrites the table's descriptors, ordered on the
         current stream."""
-        if len(grads) != len(self._tensors):
-            raise ValueError(f"{len(grads)} gradients for {len(self._tensors)} tensors")
+        if len(grads) != len(self._recs):
+            raise ValueError(f"{len(grads)} gradients for {len(self._recs)} tensors")
         bad = [g for g in grads if g is not None and (g.device != self.device or g.dtype not in _FORMAT)]
         if bad:
             raise ValueError(f"gradients belong on {self.device} in bf16, fp16 or fp32, got {bad[0].dtype} on "
                              f"{bad[0].device}")
-        before = [t["grad"] for t in self._tensors]
         self._point(grads)
         try:
-            zero_list_repoint(self._tensors, self._host, self.list)
+            zero_list_repoint(self._recs, self._host, self.list)
         except Exception:
-            self._point(before)  # the table still names them
+            self._point(self._grads)  # the table still names them
             raise
+        self._grads = list(grads)
         n = self.list.grads_bytes
         if n:
             self.table[:n].copy_(torch.frombuffer(self._host, dtype=torch.uint8, count=n))
