@@ -796,9 +796,9 @@ __device__ __forceinline__ void adamw8_block(const Desc& d, const Block8& w, con
 // (a quarter of the reductions and divisions, 104 registers) 2.13 ms and 197 us
 // at its best cap of 3; XCD groups of 8 to 96 workgroups within 1 and 2%.
 // Without the non-temporal hint on the codes 9-13% slower.  The instructions
-// have to be few: HBM leaves time for 98 issue slots an element, and a form
-// with separate reductions by shuffles, two divisions a block and correctly
-// rounded quotients took 130 of them and 3.3 ms.
+// have to be few: at this rate HBM leaves a SIMD 98 issue slots for a lane's
+// element, of which 58 are used (counters); a form with separate reductions by
+// shuffles, two divisions a block and correctly rounded quotients took 3.3 ms.
 WAVES_KERNEL(6) void list_adamw8_kernel(const Desc* __restrict__ descs, const Entry* __restrict__ entries,
                                         GroupTable host, uint64_t seed, uint64_t step,
                                         const zero_step_state* __restrict__ st,

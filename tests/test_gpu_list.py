@@ -723,3 +723,41 @@ def test_tensor_list_refusals():
     assert lst._grads[0] is g and lst._recs[0].grad == g.data_ptr()  # what the table still names is kept
     with pytest.raises(ValueError, match="gradients"):
         lst.set_grads([g, g])
+
+
+def test_a_models_parameters_step_as_torchs_optimizer():
+    """A model's own parameters and gradients (new tensors at every backward), weights decayed and biases not, clipped:
+    torch's AdamW and clip_grad_norm_ on a copy.  Both round every operation to fp32 in slightly different orders: a
+    parameter's update of about lr differs by some ten units of 2^-24 a step, its own rounding by two."""
+    torch.manual_seed(0)
+    make = lambda: torch.nn.Sequential(torch.nn.Linear(37, 129), torch.nn.GELU(), torch.nn.Linear(129, 5)).to(DEV)  # noqa: E731
+    model, copy = make(), make()
+    copy.load_state_dict(model.state_dict())
+    params, lr = list(model.parameters()), 1e-2
+    state = {k: [torch.zeros_like(p) for p in params] for k in ("master", "m", "v")}
+    for w, p in zip(state["master"], params):
+        w.copy_(p.detach())
+    opt = torch.optim.AdamW([dict(params=[p for p in copy.parameters() if p.dim() > 1], weight_decay=0.1),
+                             dict(params=[p for p in copy.parameters() if p.dim() == 1], weight_decay=0.0)], lr=lr)
+    tensors, steps = None, 4
+    for t in range(steps):
+        x = torch.randn(64, 37, device=DEV, generator=torch.Generator(DEV).manual_seed(t))
+        for net in (model, copy):
+            net.zero_grad(set_to_none=True)
+            net(x).square().mean().backward()
+        if tensors is None:
+            tensors = TensorList([p.numel() for p in params], [p.grad for p in params], params, **state,
+                                 groups=[0 if p.dim() > 1 else 1 for p in params], n_groups=2)
+            run = ListDecision(tensors, [AdamWConfig(lr=lr, weight_decay=0.1), AdamWConfig(lr=lr, weight_decay=0.0)],
+                               max_norm=0.1)
+        else:
+            tensors.set_grads([p.grad for p in params])
+        run.step()
+        norm = torch.nn.utils.clip_grad_norm_(copy.parameters(), 0.1)
+        opt.step()
+        # the two models' gradients differ by what their parameters do: the norms agree to 1e-4
+        assert run.read()["global_norm"] == pytest.approx(float(norm), rel=1e-4)
+        if t == 0:  # the same gradients on both sides
+            for p, q, w in zip(params, copy.parameters(), state["master"]):
+                assert torch.equal(p.detach(), w)
+                assert (p - q).abs().max() <= 2.0**-24 * (4 * q.abs().max() + 40 * lr)
