@@ -333,13 +333,14 @@ class TensorList:
         self._kept = (params, state, m, v)  # the table names them
         self._grads = list(grads) if grads is not None else [None] * len(numels)
         self._recs = (zero_list_tensor * len(numels))()
+        state_bytes = (zero_state8_bytes if state8 is not None else lambda n: 4 * zero_state_tiled_numel(n)
+                       if layout == ZERO_STATE_TILED else 4 * n)
         for k, rec in enumerate(self._recs):
             n = max(int(numels[k]), 0)
             rec.numel, rec.layout, rec.group = int(numels[k]), layout, groups[k] if groups is not None else 0
-            size = {ZERO_STATE_TILED: 4 * zero_state_tiled_numel(n), ZERO_STATE_8BIT: zero_state8_bytes(n)}
             if params is not None and params[k] is not None:
                 rec.param, rec.pdt = _buf(params[k], n * params[k].element_size()), _FORMAT[params[k].dtype]
-            rec.state = _buf(state[k], size.get(layout, 4 * n)) if state is not None else None
+            rec.state = _buf(state[k], state_bytes(n)) if state is not None else None
             rec.m = _buf(m[k], 4 * n) if m is not None else None
             rec.v = _buf(v[k], 4 * n) if v is not None else None
         self._point(self._grads)
