@@ -344,25 +344,27 @@ __device__ __forceinline__ bool group_scalars(const GroupTable& host, const zero
 // ------------------------------------------------------------------ norm
 
 // Adds a square, exact in fp64 (at most 2·24 significant bits), so that one
-// fused operation rounds as the product and the sum would; keeps the largest
-// magnitude pattern, which tells at the end whether any value was not finite.
-__device__ __forceinline__ void square(float x, double& acc, uint32_t& top) {
+// fused operation rounds as the product and the sum would.
+__device__ __forceinline__ void square(float x, double& acc) {
   const double d = static_cast<double>(x);
   acc = __builtin_fma(d, d, acc);
-  const uint32_t mag = __float_as_uint(x) & 0x7FFFFFFFu;
-  top = top > mag ? top : mag;
 }
+
+// A sum of squares of fp32 values is not finite exactly if one of them is not:
+// finite squares stay below 2^256, and no list is long enough to bring their
+// sum near 2^1024.
+__device__ __forceinline__ uint32_t not_finite(double sum) { return __builtin_isfinite(sum) ? 0u : 1u; }
 
 // 16 bytes of gradients: four or eight values.
 template <int DT>
-__device__ __forceinline__ void square16(u32x4 w, double& acc, uint32_t& top) {
+__device__ __forceinline__ void square16(u32x4 w, double& acc) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     if constexpr (DT == ZERO_FP32) {
-      square(__uint_as_float(w[c]), acc, top);
+      square(__uint_as_float(w[c]), acc);
     } else {
-      square(widen<DT>(w[c] & 0xFFFFu), acc, top);
-      square(widen<DT>(w[c] >> 16), acc, top);
+      square(widen<DT>(w[c] & 0xFFFFu), acc);
+      square(widen<DT>(w[c] >> 16), acc);
     }
   }
 }
@@ -371,8 +373,7 @@ __device__ __forceinline__ void square16(u32x4 w, double& acc, uint32_t& top) {
 // they start (kNormUnroll in flight per thread), then the last few elements.
 constexpr int kNormUnroll = 4;
 template <int DT, int NT>
-__device__ __forceinline__ void square_range(const void* grad, int64_t lo, int64_t hi, int thread, double& acc,
-                                             uint32_t& top) {
+__device__ __forceinline__ void square_range(const void* grad, int64_t lo, int64_t hi, int thread, double& acc) {
   constexpr int kPer = DT == ZERO_FP32 ? 4 : 8;
   const gbyte at = (gbyte)grad + lo * (16 / kPer);
   const int nv = static_cast<int>((hi - lo) / kPer);
@@ -383,44 +384,41 @@ __device__ __forceinline__ void square_range(const void* grad, int64_t lo, int64
 #pragma unroll
     for (int u = 0; u < kNormUnroll; ++u) w[u] = load(j + u * NT);
 #pragma unroll
-    for (int u = 0; u < kNormUnroll; ++u) square16<DT>(w[u], acc, top);
+    for (int u = 0; u < kNormUnroll; ++u) square16<DT>(w[u], acc);
   }
-  for (; j < nv; j += NT) square16<DT>(load(j), acc, top);
+  for (; j < nv; j += NT) square16<DT>(load(j), acc);
   const int64_t e = lo + static_cast<int64_t>(nv) * kPer + thread;
-  if (e < hi) square(load_grad1(grad, DT, e), acc, top);
+  if (e < hi) square(load_grad1(grad, DT, e), acc);
 }
 
 // The chunk of entry `en` by NT threads.
 template <int NT>
-__device__ __forceinline__ void square_chunk(const Desc* descs, Entry en, int thread, double& acc, uint32_t& top) {
+__device__ __forceinline__ void square_chunk(const Desc* descs, Entry en, int thread, double& acc) {
   const Desc d = load_desc(descs, en.tensor);
   if (d.grad == nullptr) return;
   const int64_t lo = static_cast<int64_t>(en.chunk) * kNormPer;
   const int64_t hi = lo + kNormPer < d.numel ? lo + kNormPer : d.numel;
   if (d.gdt() == ZERO_BF16) {
-    square_range<ZERO_BF16, NT>(d.grad, lo, hi, thread, acc, top);
+    square_range<ZERO_BF16, NT>(d.grad, lo, hi, thread, acc);
   } else if (d.gdt() == ZERO_FP16) {
-    square_range<ZERO_FP16, NT>(d.grad, lo, hi, thread, acc, top);
+    square_range<ZERO_FP16, NT>(d.grad, lo, hi, thread, acc);
   } else {
-    square_range<ZERO_FP32, NT>(d.grad, lo, hi, thread, acc, top);
+    square_range<ZERO_FP32, NT>(d.grad, lo, hi, thread, acc);
   }
 }
 
-constexpr uint32_t kInfBits = 0x7F800000u;
-
 // Workgroup b sums the squares of one chunk of one tensor's gradients.  Bound
 // by HBM reads: the 195M bf16 gradients of the GPT-2 rank's 47 pieces take
-// 58-62 us with the fold (6.3-6.7 TB/s), 60M fp32 ones in 500 ragged tensors
-// 38-41 us; the fold, a launch of its own, is 4.5-5 us of either.
-// Four vectors in flight per thread beat two by 6% and eight by 5%, a cap of 4
-// wavefronts per SIMD 3 by 10% and 6 by 5%; chunks of 8192 elements are 15%
-// slower, of 32,768 the same within 3%.
+// 59-61 us with the fold (6.4-6.6 TB/s), 60M fp32 ones in 500 ragged tensors
+// 38-40 us; the fold, a launch of its own, is 4.5-5 us of either.  Measured in
+// one process: two vectors in flight per thread and a cap of 8 wavefronts per
+// SIMD +4 and +5%, eight and 3 -1.5 and +2%; caps of 3, 5, 6 and 8 +2 to +4%;
+// chunks of 8192 elements +1%, 12,288 +7 and 0%, 32,768 0 and +4%.
 STREAMING_KERNEL void list_sqnorm_kernel(const Desc* __restrict__ descs, const Entry* __restrict__ entries,
                                          double* __restrict__ part_sum, uint32_t* __restrict__ part_bad) {
   double acc = 0.0;
-  uint32_t top = 0;
-  square_chunk<kBlock>(descs, entries[blockIdx.x], static_cast<int>(threadIdx.x), acc, top);
-  uint32_t bad = top >= kInfBits ? 1u : 0u;
+  square_chunk<kBlock>(descs, entries[blockIdx.x], static_cast<int>(threadIdx.x), acc);
+  uint32_t bad = not_finite(acc);
   block_reduce(acc, bad);
   if (threadIdx.x == 0) {
     part_sum[blockIdx.x] = acc;
@@ -428,22 +426,22 @@ STREAMING_KERNEL void list_sqnorm_kernel(const Desc* __restrict__ descs, const E
   }
 }
 
-// A small list in one workgroup, a wavefront to each chunk, with no partials
-// to fold: one launch instead of two.  Measured on MI355X, a call among others
-// (bf16): 65,536 elements 5.1 us against 7.8 with two launches, 131,072
-// 6.7-7.0 against 7.8-8.7, 262,144 11.1 against 7.9: up to 65,536 the launch
-// is all that it costs.
+// A small list in one workgroup, its wavefronts taking the chunks in turn, with
+// no partials to fold: one launch instead of two.  Measured on MI355X, a call
+// among others: 65,536 bf16 elements in 16 tensors 5.6 us against 8.8 with two
+// launches, 131,072 5.6 (fp32 6.0), 262,144 8.5-9.9; 40,000 in 64 and in 100
+// tensors 6.0 against 9.2, 131,072 in 128 7.3-8.4.
 constexpr int kSmallThreads = 1024;
-constexpr int64_t kSmallChunks = kSmallThreads / 64, kSmallNumel = 65536;
+constexpr int64_t kSmallChunks = 64, kSmallNumel = 131072;
 __global__ __launch_bounds__(kSmallThreads) void list_sqnorm_small_kernel(const Desc* __restrict__ descs,
                                                                           const Entry* __restrict__ entries,
                                                                           int32_t chunks, double* __restrict__ out_sum,
                                                                           int32_t* __restrict__ out_bad) {
   double acc = 0.0;
-  uint32_t top = 0;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (wave < chunks) square_chunk<64>(descs, entries[wave], static_cast<int>(threadIdx.x & 63), acc, top);
-  uint32_t bad = top >= kInfBits ? 1u : 0u;
+  for (int c = wave; c < chunks; c += kSmallThreads / 64)
+    square_chunk<64>(descs, entries[c], static_cast<int>(threadIdx.x & 63), acc);
+  uint32_t bad = not_finite(acc);
   block_reduce<kSmallThreads>(acc, bad);
   if (threadIdx.x == 0) {
     *out_sum = acc;

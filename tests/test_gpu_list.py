@@ -99,38 +99,43 @@ def bits(t):
 
 @pytest.mark.parametrize("dtype", sorted(FLOATS))
 @pytest.mark.parametrize("shift", [0, 1, 2, 3, 5])
-def test_norm(dtype, shift):
+@pytest.mark.parametrize("more", [[], [200_003], [11] * 60])  # one launch; too many elements for it; too many chunks
+def test_norm(dtype, shift, more):
     rng = np.random.default_rng(shift)
-    guard = Guarded()
-    host = [grads_host(n, FLOATS[dtype], rng) for n in SIZES]
+    guard, sizes = Guarded(), SIZES + more
+    host = [grads_host(n, FLOATS[dtype], rng) for n in sizes]
     grads = [guard(h, shift) for h in host]
     grads[7] = None  # no gradient in this step
     out = torch.zeros(2, dtype=torch.float64, device=DEV)
-    lst = TensorList(SIZES, grads)
+    lst = TensorList(sizes, grads)
     for _ in range(2):
         out.fill_(3.0)
         lst.grad_sqnorm(out[:1], out[1:].view(torch.int32))
         want = math.fsum(float(x) ** 2 for k, h in enumerate(host) if k != 7 for x in h.float())
-        got, n = float(out[0]), sum(SIZES)
+        got, n = float(out[0]), sum(sizes)
         assert abs(got - want) <= n * 2.0**-53 * want
         assert int(out[1:].view(torch.int32)[0]) == 0
     guard.check()
 
 
 @pytest.mark.parametrize("dtype", sorted(FLOATS))
-def test_norm_flags_a_non_finite_gradient_anywhere(dtype):
-    host = [torch.ones(n, dtype=FLOATS[dtype]) for n in (1, 5, 70001)]
+@pytest.mark.parametrize("one_launch", [True, False])
+def test_norm_flags_a_non_finite_gradient_anywhere(dtype, one_launch):
+    sizes = [1, 5, 70001 if one_launch else 300_001]
+    host = [torch.ones(n, dtype=FLOATS[dtype]) for n in sizes]
     out = torch.zeros(2, dtype=torch.float64, device=DEV)
     for value in (math.inf, -math.inf, math.nan):
-        for k, i in ((0, 0), (1, 4), (2, 0), (2, 16384), (2, 70000)):
+        for k, i in ((0, 0), (1, 4), (2, 0), (2, 16384), (2, sizes[2] - 1)):
             host[k][i] = value
-            TensorList([1, 5, 70001], [h.to(DEV) for h in host]).grad_sqnorm(out[:1], out[1:].view(torch.int32))
+            TensorList(sizes, [h.to(DEV) for h in host]).grad_sqnorm(out[:1], out[1:].view(torch.int32))
             assert int(out[1:].view(torch.int32)[0]) == 1, (value, k, i)
             host[k][i] = 1.0
     largest = torch.finfo(FLOATS[dtype]).max  # finite gradients whose squares stay finite in fp64
-    TensorList([4], [torch.full((4,), largest, dtype=FLOATS[dtype], device=DEV)]).grad_sqnorm(
+    n = 4 if one_launch else 2**18
+    TensorList([n], [torch.full((n,), largest, dtype=FLOATS[dtype], device=DEV)]).grad_sqnorm(
         out[:1], out[1:].view(torch.int32))
-    assert float(out[0]) == 4 * float(largest) ** 2 and int(out[1:].view(torch.int32)[0]) == 0
+    want = n * float(largest) ** 2  # 48 significant bits: sums of more than 32 of them are rounded
+    assert abs(float(out[0]) - want) <= n * 2.0**-53 * want and int(out[1:].view(torch.int32)[0]) == 0
 
 
 def test_norm_of_nothing_is_zero():
