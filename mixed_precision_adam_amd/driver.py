@@ -404,12 +404,18 @@ class TensorList:
         else:
             self._call(zero_list_adamw_step_dev, self.list, step_state, group_scalars, stream=stream)
 
+    def _same_device(self, other: "TensorList") -> None:
+        if other.device != self.device:
+            raise ValueError(f"lists on {self.device} and {other.device}: a conversion runs on one GPU")
+
     def pack8(self, target: "TensorList", stream=None) -> None:
-        """This list's fp32 state into the 8-bit state of `target` (a list of the same sizes)."""
+        """This list's fp32 state into the 8-bit state of `target` (a list of the same sizes on the same GPU)."""
+        self._same_device(target)
         self._call(zero_list_state8_pack, self.list, target.list, stream=stream)
 
     def unpack8(self, target: "TensorList", stream=None) -> None:
         """This list's 8-bit state into the fp32 state of `target`."""
+        self._same_device(target)
         self._call(zero_list_state8_unpack, self.list, target.list, stream=stream)
 
 

@@ -272,3 +272,16 @@ def test_reference_update_in_fp32_against_64_bits():
     assert (np.abs(v32 - v64) <= 10 * u * v64).all()
     step = s["step_size"] * size_m / (np.sqrt(v64) / s["bc2_sqrt"])
     assert (np.abs(p32 - p64) <= 4 * u * np.abs(args[1]) + 30 * u * step).all()
+
+
+def test_conversion_between_two_gpus_is_refused():
+    """The kernels read both lists' tables: a target on another GPU never reaches them (the lists here have no
+    plan and no memory, only their devices)."""
+    from mixed_precision_adam_amd.driver import TensorList
+
+    a, b = TensorList.__new__(TensorList), TensorList.__new__(TensorList)
+    a.device, b.device = torch.device("cuda", 0), torch.device("cuda", 1)
+    a.list = b.list = Z.zero_list()
+    for call in (a.pack8, a.unpack8, b.pack8):
+        with pytest.raises(ValueError, match="one GPU"):
+            call(b if call.__self__ is a else a)
