@@ -437,6 +437,7 @@ class ListDecision:
         self.groups = torch.zeros(12 * len(self.hparams), dtype=torch.float32, device=dev)
         with torch.cuda.device(dev):
             zero_step_state_init(self.state, loss_scale, growth_interval)
+            torch.cuda.current_stream().synchronize()  # the first step may come on any stream
 
     def step(self, stream=None) -> None:
         """Enqueues one whole step; nothing waits on the host."""

@@ -701,6 +701,25 @@ def test_two_lists_on_two_streams():
     same_blocks(y.host(0), cm, cv, sm, sv, 500_003, "second stream")
 
 
+def test_first_step_on_another_stream():
+    """A ListDecision made behind queued work steps at once on another stream as on its own."""
+    big = torch.zeros(1 << 28, device=DEV)
+    x, y = (List32([70_001], "bf16", "bf16", "tiled", 0, seed=4, groups=1) for _ in range(2))
+    cfg = [AdamWConfig(**CFG[0])]
+    plain = ListDecision(x.list, cfg, loss_scale=2.0)
+    plain.step()
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(100):
+        big.add_(1.0)
+    run = ListDecision(y.list, cfg, loss_scale=2.0)
+    run.step(stream=other)
+    torch.cuda.synchronize()
+    assert run.read() == plain.read()
+    for a, b in zip(x.held["state"], y.held["state"]):
+        assert_bits_equal(bits(a), bits(b), "state")
+
+
 def test_tensor_list_refusals():
     g = torch.zeros(8, dtype=torch.bfloat16, device=DEV)
     f = torch.zeros(8, device=DEV)
