@@ -447,7 +447,8 @@ class ListDecision:
         self.tensors.adamw_dev(self.state, self.groups, stream, self.seed)
 
     def read(self) -> dict:
-        """The decided state (synchronizes)."""
+        """The decided state of the last step queued, on whatever stream (synchronizes the device)."""
+        torch.cuda.synchronize(self.tensors.device)
         return read_step_state(self.state)
 
 

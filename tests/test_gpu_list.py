@@ -720,6 +720,20 @@ def test_first_step_on_another_stream():
         assert_bits_equal(bits(a), bits(b), "state")
 
 
+def test_state_read_after_a_step_on_another_stream():
+    """What read() gives is the queued step's, whose stream is not the current one and busy."""
+    big = torch.zeros(1 << 28, device=DEV)
+    x = List32([70_001], "bf16", "bf16", "tiled", 0, seed=4, groups=1)
+    run = ListDecision(x.list, [AdamWConfig(**CFG[0])], loss_scale=2.0)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        for _ in range(100):
+            big.add_(1.0)
+        run.step()
+    assert run.read()["adam_step"] == 1
+
+
 def test_tensor_list_refusals():
     g = torch.zeros(8, dtype=torch.bfloat16, device=DEV)
     f = torch.zeros(8, device=DEV)
