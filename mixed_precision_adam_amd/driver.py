@@ -307,7 +307,8 @@ class TensorList:
     offset, and a gradient may be None (no gradient in this step: that tensor is left as it is).  Calls run on
     the current stream of the tensors' device unless a stream is given.  The list keeps the tensors, its table and
     the norm's workspace alive: keep it until its calls are done, and give calls that may overlap in time lists of
-    their own.  A captured graph replays what the table names at the time: `set_grads` between replays is seen, and
+    their own.  It names the memory that the tensors had when it was made: parameters that get other memory
+    (``p.data = ...``) need another list.  A captured graph replays what the table names at the time: `set_grads` between replays is seen, and
     is itself not for capture."""
 
     def __init__(self, numels, grads=None, params=None, *, state=None, state8=None, master=None, m=None, v=None,
@@ -330,7 +331,7 @@ class TensorList:
                   ZERO_STATE_ARRAYS if any(x is not None for x in (master, m, v)) else ZERO_STATE_NONE)
         self.device = devices.pop() if devices else torch.device("cuda", torch.cuda.current_device())
         state = next((x for x in (state, state8, master) if x is not None), None)
-        self._kept = (params, state, m, v)  # the table names them
+        self._kept = [tuple(x) for x in (params, state, m, v) if x is not None]  # the table names these tensors
         self._grads = list(grads) if grads is not None else [None] * len(numels)
         self._recs = (zero_list_tensor * len(numels))()
         state_bytes = (zero_state8_bytes if state8 is not None else lambda n: 4 * zero_state_tiled_numel(n)

@@ -1,0 +1,116 @@
+"""TensorList and ListDecision without a GPU: what they keep alive, what they wait for and what they refuse.  The list
+entries are stand-ins with invented device addresses (nothing is launched); the table lies in host memory."""
+import gc
+import types
+import weakref
+
+import pytest
+import torch
+
+import mixed_precision_adam_amd as Z
+from mixed_precision_adam_amd import driver as D
+
+GPU = torch.device("cuda", 0)
+
+
+class OnGpu:
+    """As much of a GPU tensor as the host side looks at."""
+
+    is_cuda = True
+    next_address = 1 << 20
+
+    def __init__(self, n, dtype=torch.float32, device=GPU):
+        self.n, self.dtype, self.device = n, dtype, device
+        self.at = OnGpu.next_address
+        OnGpu.next_address += 4096 + 4 * n & ~0xFF
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.at
+
+
+class HostTorch:
+    """torch, with a list's own device memory on the host and a log of what happens to it."""
+
+    def __init__(self):
+        self.log, self.capturing = [], False
+        self.cuda = types.SimpleNamespace(synchronize=lambda device=None: self.log.append("wait for the device"),
+                                          is_current_stream_capturing=lambda: self.capturing,
+                                          current_device=lambda: 0)
+
+    def __getattr__(self, name):
+        return getattr(torch, name)
+
+    def frombuffer(self, buffer, **kw):
+        log = self.log
+
+        class Staged(torch.Tensor):
+            def to(self, device):
+                assert device == GPU
+                return Table.of(self, log)
+        return torch.frombuffer(buffer, **kw).as_subclass(Staged)
+
+    def empty(self, *size, device=None, **kw):
+        return torch.empty(*size, **kw)
+
+
+class Table:
+    """The device table."""
+
+    @staticmethod
+    def of(host, log):
+        t = Table()
+        t.bytes, t.log = bytearray(host.as_subclass(torch.Tensor).numpy().tobytes()), log
+        t.keep = torch.empty(16, dtype=torch.uint8)
+        return t
+
+    def data_ptr(self):
+        return self.keep.data_ptr()
+
+    def __getitem__(self, part):
+        table = self
+
+        class Part:
+            def copy_(self, host):
+                table.log.append("table written")
+                table.bytes[part] = host.as_subclass(torch.Tensor).numpy().tobytes()
+        return Part()
+
+
+@pytest.fixture
+def host(monkeypatch):
+    shim = HostTorch()
+    monkeypatch.setattr(D, "torch", shim)
+    return shim
+
+
+def entries(sizes, dtype=torch.float32):
+    return [OnGpu(n, dtype) for n in sizes]
+
+
+def test_the_tensors_outlive_the_callers_lists(host):
+    """Every address in the table belongs to a tensor that the list keeps, whatever becomes of the lists it was made
+    from."""
+    sizes = [8, 5000]
+    for names in (("master", "m", "v"), ("state",), ("state8",)):
+        made = {"grads": entries(sizes, torch.bfloat16), "params": entries(sizes, torch.bfloat16)}
+        for k in names:
+            made[k] = ([OnGpu(Z.zero_state8_bytes(n), torch.uint8) for n in sizes] if k == "state8" else
+                       [OnGpu(Z.zero_state_tiled_numel(n)) for n in sizes] if k == "state" else entries(sizes))
+        lst = D.TensorList(sizes, **made)
+        refs = {k: [weakref.ref(t) for t in x] for k, x in made.items()}
+        for x in made.values():
+            x[0] = None
+            x.clear()
+        gc.collect()
+        for k, x in refs.items():
+            assert all(r() is not None for r in x), k
+        del lst
