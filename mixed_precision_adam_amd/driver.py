@@ -359,24 +359,29 @@ class TensorList:
             rec.grad, rec.gdt = address, dtype
 
     def set_grads(self, grads) -> None:
-        """Other gradient tensors (or None) for the coming steps: rewrites the table's descriptors, ordered on the
-        current stream."""
+        """Other gradient tensors (or None) for the coming steps, on whatever stream: rewrites the table's descriptors
+        and lets the old gradients go.  Steps in flight read both, on streams that the list does not know (a graph's
+        replay, say), so the host waits for the device first."""
         if len(grads) != len(self._recs):
             raise ValueError(f"{len(grads)} gradients for {len(self._recs)} tensors")
         bad = [g for g in grads if g is not None and (g.device != self.device or g.dtype not in _FORMAT)]
         if bad:
             raise ValueError(f"gradients belong on {self.device} in bf16, fp16 or fp32, got {bad[0].dtype} on "
                              f"{bad[0].device}")
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("set_grads cannot be captured: the table is written from the host")
         self._point(grads)
         try:
             zero_list_repoint(self._recs, self._host, self.list)
+            torch.cuda.synchronize(self.device)
+            n = self.list.grads_bytes
+            if n:  # a copy from pageable memory: in place when it returns
+                self.table[:n].copy_(torch.frombuffer(self._host, dtype=torch.uint8, count=n))
         except Exception:
-            self._point(self._grads)  # the table still names them
+            self._point(self._grads)  # the device's table still names them
+            zero_list_repoint(self._recs, self._host, self.list)
             raise
         self._grads = list(grads)
-        n = self.list.grads_bytes
-        if n:
-            self.table[:n].copy_(torch.frombuffer(self._host, dtype=torch.uint8, count=n))
 
     def _call(self, fn, *args, stream=None) -> None:
         if stream is None:

@@ -114,3 +114,65 @@ def test_the_tensors_outlive_the_callers_lists(host):
         for k, x in refs.items():
             assert all(r() is not None for r in x), k
         del lst
+
+
+def grads_of(table, n):
+    """The gradient addresses that a table names."""
+    return [int.from_bytes(table.bytes[64 * k:64 * k + 8], "little") for k in range(n)]
+
+
+def test_new_gradients_wait_for_steps_in_flight(host):
+    """A step queued on any stream, or a graph's replay, reads the table and the gradients that it names: the table is
+    rewritten and the old gradients are let go only when the device is idle."""
+    sizes = [8, 5000]
+    lst = D.TensorList(sizes, entries(sizes), entries(sizes), master=entries(sizes), m=entries(sizes),
+                       v=entries(sizes))
+    old = [weakref.ref(g) for g in lst._grads]
+    alive_at = []
+
+    class Watched(list):
+        def append(self, what):
+            alive_at.append((what, all(r() is not None for r in old)))
+    for target in (host, lst.table):
+        target.log = Watched()
+    new = entries(sizes, torch.bfloat16)
+    lst.set_grads(new)
+    assert alive_at == [("wait for the device", True), ("table written", True)]
+    gc.collect()
+    assert all(r() is None for r in old)
+    assert grads_of(lst.table, 2) == [g.at for g in new]
+
+
+def test_new_gradients_are_refused_while_capturing(host):
+    sizes = [8, 5000]
+    lst = D.TensorList(sizes, entries(sizes))
+    before, named = list(lst._grads), bytes(lst.table.bytes)
+    host.log.clear()
+    host.capturing = True
+    with pytest.raises(RuntimeError, match="captur"):
+        lst.set_grads(entries(sizes))
+    assert host.log == [] and lst._grads == before and bytes(lst.table.bytes) == named
+    assert [r.grad for r in lst._recs] == [g.at for g in before]
+
+
+def test_gradients_that_the_device_never_got_are_not_taken(host):
+    """An error of the wait or of the copy leaves the list with the gradients that the device's table names."""
+    sizes = [8, 5000]
+    for failing in ("wait", "copy"):
+        lst = D.TensorList(sizes, entries(sizes))
+        before, staged = list(lst._grads), bytes(lst._host)
+
+        def fails(*args):
+            raise RuntimeError("device error")
+
+        class Failing(list):
+            append = fails
+        if failing == "wait":
+            host.cuda.synchronize = fails
+        else:
+            host.cuda.synchronize = lambda device=None: None
+            lst.table.log = Failing()
+        with pytest.raises(RuntimeError, match="device error"):
+            lst.set_grads([None, OnGpu(5000)])
+        assert lst._grads == before and bytes(lst._host) == staged, failing
+        assert [r.grad for r in lst._recs] == [g.at for g in before]
