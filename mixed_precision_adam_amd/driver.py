@@ -427,16 +427,21 @@ class TensorList:
 
 class ListDecision:
     """Device-resident steps over a TensorList: norm, decision (with the scalars of every group) and update are
-    queued back to back with no host round trip, and can be captured in a HIP graph."""
+    queued back to back with no host round trip, and can be captured in a HIP graph.  `cfgs`: one AdamWConfig for each
+    group.  One norm over all of them is clipped, to their max_norm (the same in each) unless `max_norm` is given."""
 
-    def __init__(self, tensors: TensorList, cfgs, max_norm: float = 1.0, loss_scale: float = 1.0,
+    def __init__(self, tensors: TensorList, cfgs, max_norm: float | None = None, loss_scale: float = 1.0,
                  growth_interval: int = 2**31 - 1, seed: int = 0):
         dev = tensors.device
-        self.tensors, self.max_norm, self.seed = tensors, max_norm, seed
+        self.tensors, self.seed = tensors, seed
         self.hparams = zero_list_hparams([dict(lr=c.lr, beta1=c.beta1, beta2=c.beta2, eps=c.eps,
                                                weight_decay=c.weight_decay) for c in cfgs])
         if len(self.hparams) != tensors.list.n_groups:
             raise ValueError(f"{len(self.hparams)} configurations for {tensors.list.n_groups} groups")
+        norms = {c.max_norm for c in cfgs} if max_norm is None else {max_norm}
+        if len(norms) != 1:
+            raise ValueError(f"the groups' configurations differ in max_norm ({sorted(norms)}): give one as an argument")
+        self.max_norm = norms.pop()
         self.norms = torch.zeros(2, dtype=torch.float64, device=dev)  # square-norm, then its flag
         self._sq, self._flag = self.norms.data_ptr(), self.norms.data_ptr() + 8
         self.state = torch.zeros(16, dtype=torch.float64, device=dev)

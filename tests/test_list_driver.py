@@ -1,5 +1,6 @@
 """TensorList and ListDecision without a GPU: what they keep alive, what they wait for and what they refuse.  The list
 entries are stand-ins with invented device addresses (nothing is launched); the table lies in host memory."""
+import contextlib
 import gc
 import types
 import weakref
@@ -44,7 +45,8 @@ class HostTorch:
         self.log, self.capturing = [], False
         self.cuda = types.SimpleNamespace(synchronize=lambda device=None: self.log.append("wait for the device"),
                                           is_current_stream_capturing=lambda: self.capturing,
-                                          current_device=lambda: 0)
+                                          current_device=lambda: 0, device=contextlib.nullcontext,
+                                          current_stream=lambda: types.SimpleNamespace(synchronize=lambda: None))
 
     def __getattr__(self, name):
         return getattr(torch, name)
@@ -60,6 +62,9 @@ class HostTorch:
 
     def empty(self, *size, device=None, **kw):
         return torch.empty(*size, **kw)
+
+    def zeros(self, *size, device=None, **kw):
+        return torch.zeros(*size, **kw)
 
 
 class Table:
@@ -90,6 +95,22 @@ def host(monkeypatch):
     shim = HostTorch()
     monkeypatch.setattr(D, "torch", shim)
     return shim
+
+
+@pytest.fixture
+def queued(host, monkeypatch):
+    """The calls that a step queues, by name, with what the decision was given: (max_norm, every group's settings)."""
+    calls = []
+    monkeypatch.setattr(D, "_current_raw_stream", lambda index: 0)
+    monkeypatch.setattr(D, "zero_step_state_init", lambda *args: None)
+
+    def decision(sq, flags, ranks, max_norm, hparams, state, groups, stream):
+        calls.append(("decision", max_norm, [(h.lr, h.beta1, h.beta2, h.eps, h.weight_decay) for h in hparams]))
+    monkeypatch.setattr(D, "zero_list_grad_sqnorm", lambda *args: calls.append(("norm",)))
+    monkeypatch.setattr(D, "zero_list_decision_dev", decision)
+    for name in ("zero_list_adamw_step_dev", "zero_list_adamw8_step_dev"):
+        monkeypatch.setattr(D, name, lambda *args: calls.append(("update",)))
+    return calls
 
 
 def entries(sizes, dtype=torch.float32):
@@ -176,3 +197,24 @@ def test_gradients_that_the_device_never_got_are_not_taken(host):
             lst.set_grads([None, OnGpu(5000)])
         assert lst._grads == before and bytes(lst._host) == staged, failing
         assert [r.grad for r in lst._recs] == [g.at for g in before]
+
+
+def whole(sizes, n_groups=1):
+    return D.TensorList(sizes, entries(sizes), entries(sizes), master=entries(sizes), m=entries(sizes),
+                        v=entries(sizes), groups=[k % n_groups for k in range(len(sizes))], n_groups=n_groups)
+
+
+def test_clipping_is_the_configurations(queued):
+    """max_norm as DeviceDecision takes it, from the configuration; an argument of its own goes first."""
+    def clipped(*cfgs, **kw):
+        queued.clear()
+        D.ListDecision(whole([8, 5000], len(cfgs)), list(cfgs), **kw).step()
+        return queued[1][1]
+    assert clipped(D.AdamWConfig()) == D.AdamWConfig().max_norm
+    for norm in (0.0, 0.1, 2.0):
+        assert clipped(D.AdamWConfig(max_norm=norm)) == norm
+        assert clipped(D.AdamWConfig(max_norm=norm), D.AdamWConfig(lr=1.0, max_norm=norm)) == norm
+        assert clipped(D.AdamWConfig(max_norm=0.3), max_norm=norm) == norm
+    assert clipped(D.AdamWConfig(max_norm=0.1), D.AdamWConfig(max_norm=0.2), max_norm=0.5) == 0.5
+    with pytest.raises(ValueError, match="max_norm"):
+        clipped(D.AdamWConfig(max_norm=0.1), D.AdamWConfig(max_norm=0.2))
