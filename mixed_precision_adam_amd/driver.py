@@ -18,12 +18,12 @@ import numpy as np
 import torch
 
 from . import (ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO_STATE_8BIT, ZERO_STATE_ARRAYS, ZERO_STATE_NONE, ZERO_STATE_TILE,
-               ZERO_STATE_TILED, _buf, read_step_state, zero_adamw_step, zero_adamw_step_dev, zero_adamw_step_tiled,
-               zero_adamw_step_tiled_dev, zero_bucket_segments, zero_flatten_grads, zero_flatten_grads_partials,
-               zero_flatten_grads_sqnorm, zero_flatten_partials_count, zero_flatten_plan, zero_grad_sqnorm,
-               zero_grad_sqnorm_workspace_bytes, zero_list_adamw8_step, zero_list_adamw8_step_dev,
-               zero_list_adamw_step, zero_list_adamw_step_dev, zero_list_decision_dev, zero_list_grad_sqnorm,
-               zero_list_grad_sqnorm_workspace_bytes, zero_list_hparams, zero_list_plan, zero_list_repoint,
+               ZERO_STATE_TILED, _buf, read_step_state, zero_adamw_hparams, zero_adamw_step, zero_adamw_step_dev,
+               zero_adamw_step_tiled, zero_adamw_step_tiled_dev, zero_bucket_segments, zero_flatten_grads,
+               zero_flatten_grads_partials, zero_flatten_grads_sqnorm, zero_flatten_partials_count,
+               zero_flatten_plan, zero_grad_sqnorm, zero_grad_sqnorm_workspace_bytes, zero_list_adamw8_step,
+               zero_list_adamw8_step_dev, zero_list_adamw_step, zero_list_adamw_step_dev, zero_list_decision_dev,
+               zero_list_grad_sqnorm, zero_list_grad_sqnorm_workspace_bytes, zero_list_plan, zero_list_repoint,
                zero_list_state8_pack, zero_list_state8_unpack, zero_list_tensor, zero_shard_layout, zero_sqnorm_reduce,
                zero_state8_bytes, zero_state_tile, zero_state_tiled_numel, zero_state_untile, zero_step_decision,
                zero_step_decision_dev, zero_step_state_init)
@@ -428,20 +428,19 @@ class TensorList:
 class ListDecision:
     """Device-resident steps over a TensorList: norm, decision (with the scalars of every group) and update are
     queued back to back with no host round trip, and can be captured in a HIP graph.  `cfgs`: one AdamWConfig for each
-    group.  One norm over all of them is clipped, to their max_norm (the same in each) unless `max_norm` is given."""
+    group, read at every step (a captured step keeps those of its capture).  One norm over all of them is clipped, to
+    their max_norm (the same in each) unless `max_norm` is given."""
 
     def __init__(self, tensors: TensorList, cfgs, max_norm: float | None = None, loss_scale: float = 1.0,
                  growth_interval: int = 2**31 - 1, seed: int = 0):
         dev = tensors.device
         self.tensors, self.seed = tensors, seed
-        self.hparams = zero_list_hparams([dict(lr=c.lr, beta1=c.beta1, beta2=c.beta2, eps=c.eps,
-                                               weight_decay=c.weight_decay) for c in cfgs])
-        if len(self.hparams) != tensors.list.n_groups:
-            raise ValueError(f"{len(self.hparams)} configurations for {tensors.list.n_groups} groups")
-        norms = {c.max_norm for c in cfgs} if max_norm is None else {max_norm}
-        if len(norms) != 1:
-            raise ValueError(f"the groups' configurations differ in max_norm ({sorted(norms)}): give one as an argument")
-        self.max_norm = norms.pop()
+        self.cfgs, self._norm_given = list(cfgs), max_norm is not None
+        if len(self.cfgs) != tensors.list.n_groups:
+            raise ValueError(f"{len(self.cfgs)} configurations for {tensors.list.n_groups} groups")
+        self.max_norm, self._seen, self._seen_norms = max_norm, [None] * len(self.cfgs), None
+        self.hparams = (zero_adamw_hparams * len(self.cfgs))()
+        self._follow()
         self.norms = torch.zeros(2, dtype=torch.float64, device=dev)  # square-norm, then its flag
         self._sq, self._flag = self.norms.data_ptr(), self.norms.data_ptr() + 8
         self.state = torch.zeros(16, dtype=torch.float64, device=dev)
@@ -450,8 +449,23 @@ class ListDecision:
             zero_step_state_init(self.state, loss_scale, growth_interval)
             torch.cuda.current_stream().synchronize()  # the first step may come on any stream
 
+    def _follow(self) -> None:
+        """Takes over what changed in the configurations since it last looked."""
+        if not self._norm_given:
+            norms = [c.max_norm for c in self.cfgs]
+            if norms != self._seen_norms:
+                if len(set(norms)) != 1:
+                    raise ValueError(f"the groups' configurations differ in max_norm ({norms}): give one as an argument")
+                self.max_norm, self._seen_norms = norms[0], norms
+        for k, c in enumerate(self.cfgs):
+            now = (c.lr, c.beta1, c.beta2, c.eps, c.weight_decay)
+            if now != self._seen[k]:
+                self.hparams[k] = zero_adamw_hparams(*now, 1.0, 1)
+                self._seen[k] = now
+
     def step(self, stream=None) -> None:
-        """Enqueues one whole step; nothing waits on the host."""
+        """Enqueues one whole step with the configurations as they are now; nothing waits on the host."""
+        self._follow()
         self.tensors.grad_sqnorm(self._sq, self._flag, stream)
         self.tensors._call(zero_list_decision_dev, self._sq, self._flag, 1, self.max_norm, self.hparams, self.state,
                            self.groups, stream=stream)

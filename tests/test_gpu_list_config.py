@@ -44,3 +44,14 @@ def test_clipping(max_norm):
     for _ in range(2):
         got = both.step()
         assert (got["grad_scale"] == 1.0) == (max_norm == 0.0)
+
+
+def test_a_schedule():
+    """lr and max_norm set between steps."""
+    cfg = AdamWConfig(lr=1e-3)
+    both = Both(cfg)
+    for lr, norm in ((1e-3, 1.0), (5e-4, 1.0), (2e-4, 0.5)):
+        cfg.lr, cfg.max_norm = lr, norm
+        got = both.step()
+        step, t = got["scalars"][6], got["adam_step"]
+        assert step == pytest.approx(lr / (1 - 0.9**t), rel=1e-6)  # one rounding to fp32: 2^-24

@@ -218,3 +218,47 @@ def test_clipping_is_the_configurations(queued):
     assert clipped(D.AdamWConfig(max_norm=0.1), D.AdamWConfig(max_norm=0.2), max_norm=0.5) == 0.5
     with pytest.raises(ValueError, match="max_norm"):
         clipped(D.AdamWConfig(max_norm=0.1), D.AdamWConfig(max_norm=0.2))
+
+
+def test_a_changed_configuration_is_the_next_steps(queued):
+    """A learning-rate schedule sets cfg.lr between steps, as with DeviceDecision, which reads its configuration at
+    every step.  What a program sets in `hparams` or `max_norm` itself stays until the configuration changes."""
+    cfgs = [D.AdamWConfig(lr=1e-3), D.AdamWConfig(lr=2e-3, weight_decay=0.0)]
+    run = D.ListDecision(whole([8, 5000], 2), cfgs)
+
+    def step():
+        queued.clear()
+        run.step()
+        assert [c[0] for c in queued] == ["norm", "decision", "update"]
+        return queued[1]
+
+    def want(norm):
+        return ("decision", norm, [(c.lr, c.beta1, c.beta2, c.eps, c.weight_decay) for c in cfgs])
+    assert step() == want(1.0)
+    cfgs[0].lr = 5e-4
+    assert step() == want(1.0)
+    cfgs[1].beta1, cfgs[1].beta2, cfgs[1].eps, cfgs[1].weight_decay = 0.8, 0.95, 1e-6, 0.2
+    assert step() == want(1.0)
+    for c in cfgs:
+        c.max_norm = 0.25
+    assert step() == want(0.25)
+    run.hparams[0].lr, run.max_norm = 7e-4, 0.5
+    _, norm, groups = step()
+    assert norm == 0.5 and groups[0][0] == 7e-4
+    cfgs[0].lr = 1e-4
+    assert step() == want(0.5)
+    cfgs[0].max_norm = 0.125
+    queued.clear()
+    with pytest.raises(ValueError, match="max_norm"):
+        run.step()
+    assert queued == []
+    cfgs[1].max_norm = 0.125
+    assert step() == want(0.125)
+
+
+def test_a_given_max_norm_stays(queued):
+    cfg = D.AdamWConfig(max_norm=0.1)
+    run = D.ListDecision(whole([8]), [cfg], max_norm=0.5)
+    cfg.max_norm, cfg.lr = 0.2, 3e-4
+    run.step()
+    assert queued[1][1] == 0.5 and queued[1][2][0][0] == 3e-4
