@@ -386,14 +386,22 @@ class TensorList:
     def _call(self, fn, *args, stream=None) -> None:
         if stream is None:
             stream = _current_raw_stream(self.device.index)
+        elif not isinstance(stream, int) and stream.device != self.device:
+            raise ValueError(f"a stream of {stream.device} for a list on {self.device}")
         if torch.cuda.current_device() == self.device.index:
             fn(*args, stream)
         else:  # kernels are launched from the device that holds the tensors
             with torch.cuda.device(self.device):
                 fn(*args, stream)
 
+    def _here(self, *buffers) -> None:
+        for t in buffers:
+            if not isinstance(t, int) and t.device != self.device:
+                raise ValueError(f"a buffer on {t.device} for a list on {self.device}")
+
     def grad_sqnorm(self, sqnorm_out, nonfinite_out, stream=None) -> None:
         """fp64 sum of squares and inf/NaN flag over every gradient."""
+        self._here(sqnorm_out, nonfinite_out)
         self._call(zero_list_grad_sqnorm, self.list, self.ws, self.ws_bytes, sqnorm_out, nonfinite_out, stream=stream)
 
     def adamw(self, hparams, stream=None, seed: int = 0) -> None:
@@ -405,6 +413,7 @@ class TensorList:
 
     def adamw_dev(self, step_state, group_scalars, stream=None, seed: int = 0) -> None:
         """The update with the scalars of zero_list_decision_dev."""
+        self._here(step_state, group_scalars)
         if self.state8:
             self._call(zero_list_adamw8_step_dev, self.list, step_state, group_scalars, seed, stream=stream)
         else:

@@ -63,8 +63,8 @@ class HostTorch:
     def empty(self, *size, device=None, **kw):
         return torch.empty(*size, **kw)
 
-    def zeros(self, *size, device=None, **kw):
-        return torch.zeros(*size, **kw)
+    def zeros(self, n, dtype=torch.float32, device=None):
+        return OnGpu(n, dtype, device)
 
 
 class Table:
@@ -262,3 +262,27 @@ def test_a_given_max_norm_stays(queued):
     cfg.max_norm, cfg.lr = 0.2, 3e-4
     run.step()
     assert queued[1][1] == 0.5 and queued[1][2][0][0] == 3e-4
+
+
+def test_buffers_and_streams_of_another_gpu_are_refused(host, queued):
+    """The kernels run on the list's GPU: an output, a step state or a stream of another one never reaches them."""
+    there = torch.device("cuda", 1)
+    lst = whole([8, 5000])
+    sq, flag = OnGpu(1, torch.float64), OnGpu(1, torch.int32)
+    state, groups = OnGpu(16, torch.float64), OnGpu(12)
+    far = {x: OnGpu(x.n, x.dtype, there) for x in (sq, flag, state, groups)}
+    stream = types.SimpleNamespace(cuda_stream=0, device=there)
+    for call in (lambda: lst.grad_sqnorm(far[sq], flag), lambda: lst.grad_sqnorm(sq, far[flag]),
+                 lambda: lst.adamw_dev(far[state], groups), lambda: lst.adamw_dev(state, far[groups]),
+                 lambda: lst.grad_sqnorm(sq, flag, stream), lambda: lst.adamw_dev(state, groups, stream=stream),
+                 lambda: lst.adamw(None, stream=stream), lambda: lst.pack8(lst, stream=stream),
+                 lambda: lst.unpack8(lst, stream=stream),
+                 lambda: D.ListDecision(lst, [D.AdamWConfig()]).step(stream)):
+        with pytest.raises(ValueError, match="cuda:1"):
+            call()
+    assert queued == []
+    near = types.SimpleNamespace(cuda_stream=0, device=GPU)
+    lst.grad_sqnorm(sq, flag, near)
+    lst.adamw_dev(state, groups, near)
+    lst.grad_sqnorm(sq.at, flag.at, 0)
+    assert len(queued) == 3
