@@ -17,16 +17,17 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO_STATE_8BIT, ZERO_STATE_ARRAYS, ZERO_STATE_NONE, ZERO_STATE_TILE,
-               ZERO_STATE_TILED, _buf, read_step_state, zero_adamw_hparams, zero_adamw_step, zero_adamw_step_dev,
-               zero_adamw_step_tiled, zero_adamw_step_tiled_dev, zero_bucket_segments, zero_flatten_grads,
-               zero_flatten_grads_partials, zero_flatten_grads_sqnorm, zero_flatten_partials_count,
-               zero_flatten_plan, zero_grad_sqnorm, zero_grad_sqnorm_workspace_bytes, zero_list_adamw8_step,
-               zero_list_adamw8_step_dev, zero_list_adamw_step, zero_list_adamw_step_dev, zero_list_decision_dev,
-               zero_list_grad_sqnorm, zero_list_grad_sqnorm_workspace_bytes, zero_list_plan, zero_list_repoint,
-               zero_list_state8_pack, zero_list_state8_unpack, zero_list_tensor, zero_shard_layout, zero_sqnorm_reduce,
-               zero_state8_bytes, zero_state_tile, zero_state_tiled_numel, zero_state_untile, zero_step_decision,
-               zero_step_decision_dev, zero_step_state_init)
+from . import (ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO_LIST_HAS_PARAMS, ZERO_LIST_WHOLE_STATE, ZERO_STATE_8BIT,
+               ZERO_STATE_ARRAYS, ZERO_STATE_NONE, ZERO_STATE_TILE, ZERO_STATE_TILED, _buf, read_step_state,
+               zero_adamw_hparams, zero_adamw_step, zero_adamw_step_dev, zero_adamw_step_tiled,
+               zero_adamw_step_tiled_dev, zero_bucket_segments, zero_flatten_grads, zero_flatten_grads_partials,
+               zero_flatten_grads_sqnorm, zero_flatten_partials_count, zero_flatten_plan, zero_grad_sqnorm,
+               zero_grad_sqnorm_workspace_bytes, zero_list_adamw8_step, zero_list_adamw8_step_dev,
+               zero_list_adamw_step, zero_list_adamw_step_dev, zero_list_decision_dev, zero_list_grad_sqnorm,
+               zero_list_grad_sqnorm_workspace_bytes, zero_list_plan, zero_list_repoint, zero_list_state8_pack,
+               zero_list_state8_unpack, zero_list_tensor, zero_shard_layout, zero_sqnorm_reduce, zero_state8_bytes,
+               zero_state_tile, zero_state_tiled_numel, zero_state_untile, zero_step_decision, zero_step_decision_dev,
+               zero_step_state_init)
 
 _FORMAT = {torch.bfloat16: ZERO_BF16, torch.float16: ZERO_FP16, torch.float32: ZERO_FP32}
 _TORCH16 = {ZERO_BF16: torch.bfloat16, ZERO_FP16: torch.float16}
@@ -447,6 +448,9 @@ class ListDecision:
         self.cfgs, self._norm_given = list(cfgs), max_norm is not None
         if len(self.cfgs) != tensors.list.n_groups:
             raise ValueError(f"{len(self.cfgs)} configurations for {tensors.list.n_groups} groups")
+        whole = ZERO_LIST_HAS_PARAMS | ZERO_LIST_WHOLE_STATE
+        if tensors.list.n_tensors and (tensors.list.state == 0 or tensors.list.flags & whole != whole):
+            raise ValueError("a step needs a param, a master and both moments for every tensor")
         self.max_norm, self._seen, self._seen_norms = max_norm, [None] * len(self.cfgs), None
         self.hparams = (zero_adamw_hparams * len(self.cfgs))()
         self._follow()

@@ -286,3 +286,18 @@ def test_buffers_and_streams_of_another_gpu_are_refused(host, queued):
     lst.adamw_dev(state, groups, near)
     lst.grad_sqnorm(sq.at, flag.at, 0)
     assert len(queued) == 3
+
+
+def test_steps_need_a_list_that_the_update_takes(queued):
+    """Refused when made: at a step, the decision would have been queued (and counted) before the update's refusal."""
+    sizes = [8, 5000]
+    e = entries
+    for lst in (D.TensorList(sizes, e(sizes)), D.TensorList(sizes, e(sizes), e(sizes)),
+                D.TensorList(sizes, e(sizes), master=e(sizes), m=e(sizes), v=e(sizes)),
+                D.TensorList(sizes, e(sizes), e(sizes), master=e(sizes), m=e(sizes)),
+                D.TensorList(sizes, e(sizes), [OnGpu(8), None], master=e(sizes), m=e(sizes), v=e(sizes))):
+        with pytest.raises(ValueError, match="param"):
+            D.ListDecision(lst, [D.AdamWConfig()])
+    for lst in (whole(sizes), D.TensorList([], []), D.TensorList(sizes, e(sizes), e(sizes), state8=[
+            OnGpu(Z.zero_state8_bytes(n), torch.uint8) for n in sizes])):
+        D.ListDecision(lst, [D.AdamWConfig()]).step()
