@@ -395,10 +395,11 @@ class TensorList:
             with torch.cuda.device(self.device):
                 fn(*args, stream)
 
-    def _here(self, *buffers) -> None:
-        for t in buffers:
-            if not isinstance(t, int) and t.device != self.device:
-                raise ValueError(f"a buffer on {t.device} for a list on {self.device}")
+    def _here(self, a, b) -> None:
+        at = self.device.index
+        if not ((isinstance(a, int) or a.get_device() == at) and (isinstance(b, int) or b.get_device() == at)):
+            raise ValueError(f"buffers on {' and '.join(str(t.device) for t in (a, b) if not isinstance(t, int))} for "
+                             f"a list on {self.device}")
 
     def grad_sqnorm(self, sqnorm_out, nonfinite_out, stream=None) -> None:
         """fp64 sum of squares and inf/NaN flag over every gradient."""

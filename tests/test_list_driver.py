@@ -31,6 +31,9 @@ class OnGpu:
     def element_size(self):
         return self.dtype.itemsize
 
+    def get_device(self):
+        return self.device.index
+
     def is_contiguous(self):
         return True
 
