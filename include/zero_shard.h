@@ -437,10 +437,11 @@ enum {
  * finite (a step whose norm flagged it is to be skipped, as ever).  Packing
  * takes the magnitude of a v.
  *   Updates round stochastically: position p between two codes k and k+1 goes
- * to k+1 with probability p - k, so the expected value is the value.  With
- * rounding to nearest the second moment would stand still: a step changes it
- * by a factor of 1 - beta2 or less, far below half the distance of two codes
- * (3 to 6%).  The dither is a counter hash, the same for the same arguments:
+ * to k+1 with probability p - k, so the expected value is the value, except for
+ * a v below code 1 that is not zero, which is held as code 1.  With rounding to
+ * nearest the second moment could grow but never decay: a step shrinks it by
+ * at most 1 - beta2 of itself (0.1% at beta2 = 0.999), far below half the
+ * distance of two codes (3 to 6%).  The dither is a counter hash, the same for the same arguments:
  *   base = mix(seed + G·t), key(b) = mix(base + G·(b + 1)), all mod 2^64,
  *   mix = SplitMix64's output function, G = 0x9E3779B97F4A7C15, t the Adam step,
  *   b = the block's number in the list (every tensor counts whole tiles: 16
@@ -454,7 +455,8 @@ int64_t zero_state8_bytes(int64_t n);
 
 /* One tensor (or piece) of a list. */
 typedef struct zero_list_tensor {
-  const void* grad;  /* numel gradients in format gdt; NULL: no gradient in this step, the tensor is left as it is */
+  const void* grad;  /* numel gradients in format gdt; NULL: no gradient in this step, the tensor is left as it is
+                      * (Adam's t is the list's, not the tensor's: it counts the step all the same) */
   void* param;       /* numel parameters in format pdt, written by the updates (never read); NULL: none */
   void* state;       /* see the layouts above */
   float* m;          /* ZERO_STATE_ARRAYS only */

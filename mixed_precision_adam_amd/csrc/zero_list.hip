@@ -459,7 +459,7 @@ __global__ __launch_bounds__(kSmallThreads) void list_sqnorm_small_kernel(const 
 // and parameters: the 195M parameters of the GPT-2 rank's pieces (tiled) take
 // 823-829 us (6.6 TB/s, the flat update's rate: the two table lookups ahead of
 // the data hide behind the other workgroups), 60M in 500 ragged tensors off the
-// 16-byte lines (arrays) 274 us (6.1 TB/s).  Measured in one process on the
+// 16-byte lines (arrays) 271-275 us (6.1-6.2 TB/s).  Measured in one process on the
 // Llama-7B rank's 842M (tiled, 3.59 ms) and on the ragged ones: 3 wavefronts
 // per SIMD -0.5% and +1.7%, 5 +0.8% and +2.8%, 8 +2.1% and +4.2%; launches of
 // 2^24 elements +1.5% and +1.9%, of 2^26 +0.4% and -0.1%.
@@ -710,9 +710,11 @@ __device__ __forceinline__ void store_scales(const Block8& w, float scale) {
 // bit for bit, and its parameter but for rounding: the root and the quotients
 // are the hardware's approximations (1 ulp each) and two products are fused
 // with their sums.  That changes the step p takes by at most 14·2^-24 of
-// itself, where the moments it is made of carry four bits, and the update runs
-// 4% faster than with correctly rounded ones (2.30 against 2.40 ms with four
-// blocks a wavefront, 842M parameters).
+// itself, where the moments it is made of carry four bits.  Measured in one
+// process: with adam_element's correctly rounded ones the update takes 2.45
+// instead of 2.07 ms (842M parameters) and 196 instead of 188 us (60M ragged
+// fp32 ones), and at the best occupancy cap for each 2.39 ms (8 wavefronts per
+// SIMD) and 193 us (7).
 __device__ __forceinline__ void adam8_element(float g, float& p, float& m, float& v, const AdamScalars& s,
                                               float inv_bc2) {
   g = g * s.gscale;
@@ -895,7 +897,7 @@ __device__ __forceinline__ void unpack_wave(const Desc* descs32, const Desc* des
 //   unpack of master and moments: one block, 3 per SIMD 545 us (6.4 TB/s) for
 //     195M and 174 us for 60M, 4 576 and 172; four blocks at 4 595 and 186;
 //   unpack of moments alone: four blocks, 2 per SIMD 1.36 ms (6.2 TB/s) for
-//     842M and 95 us for 60M, at 4 1.47 and 108; one block at 3 and 4
+//     842M and 95-97 us for 60M, at 4 1.47 and 108; one block at 3 and 4
 //     1.83-2.18 and 124-147, at 8 1.47 and 104.  Lists of few tiles (one per
 //     compute unit) take the one-block form here too: 40,000 elements 3.2 us
 //     on the GPU against 4.6.

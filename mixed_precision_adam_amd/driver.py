@@ -305,7 +305,8 @@ class TensorList:
     """A planned list of tensors: gradients read and parameters written where they lie, with fp32 state
     (``state`` tiled, or ``master``/``m``/``v``), 8-bit state (``state8``) or none (norm only).  Every argument is
     a list with one contiguous GPU tensor per list entry; ``grads`` and ``params`` may hold views at any element
-    offset, and a gradient may be None (no gradient in this step: that tensor is left as it is).  Calls run on
+    offset, and a gradient may be None (no gradient in this step: that tensor is left as it is, though the step
+    counts for its bias correction, which has one count for the whole list).  Calls run on
     the current stream of the tensors' device unless a stream is given.  The list keeps the tensors, its table and
     the norm's workspace alive: keep it until its calls are done, and give calls that may overlap in time lists of
     their own.  It names the memory that the tensors had when it was made: parameters that get other memory
@@ -426,12 +427,13 @@ class TensorList:
             raise ValueError(f"lists on {self.device} and {other.device}: a conversion runs on one GPU")
 
     def pack8(self, target: "TensorList", stream=None) -> None:
-        """This list's fp32 state into the 8-bit state of `target` (a list of the same sizes on the same GPU)."""
+        """This list's fp32 state into the 8-bit state of `target` (a list of the same sizes on the same GPU); of
+        master, m and v, one that this list does not have becomes zeros there."""
         self._same_device(target)
         self._call(zero_list_state8_pack, self.list, target.list, stream=stream)
 
     def unpack8(self, target: "TensorList", stream=None) -> None:
-        """This list's 8-bit state into the fp32 state of `target`."""
+        """This list's 8-bit state into the fp32 state of `target`: those of master, m and v that it has."""
         self._same_device(target)
         self._call(zero_list_state8_unpack, self.list, target.list, stream=stream)
 
