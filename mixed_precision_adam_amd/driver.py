@@ -30,6 +30,7 @@ from . import (ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO_LIST_HAS_PARAMS, ZERO_LIST_
                zero_step_state_init)
 
 _FORMAT = {torch.bfloat16: ZERO_BF16, torch.float16: ZERO_FP16, torch.float32: ZERO_FP32}
+_ADDRESS = (int, type(None))  # what a call takes in place of a tensor
 _TORCH16 = {ZERO_BF16: torch.bfloat16, ZERO_FP16: torch.float16}
 
 
@@ -302,16 +303,16 @@ class BucketPipeline:
 
 
 class TensorList:
-    """A planned list of tensors: gradients read and parameters written where they lie, with fp32 state
-    (``state`` tiled, or ``master``/``m``/``v``), 8-bit state (``state8``) or none (norm only).  Every argument is
-    a list with one contiguous GPU tensor per list entry; ``grads`` and ``params`` may hold views at any element
-    offset, and a gradient may be None (no gradient in this step: that tensor is left as it is, though the step
-    counts for its bias correction, which has one count for the whole list).  Calls run on
-    the current stream of the tensors' device unless a stream is given.  The list keeps the tensors, its table and
-    the norm's workspace alive: keep it until its calls are done, and give calls that may overlap in time lists of
-    their own.  It names the memory that the tensors had when it was made: parameters that get other memory
-    (``p.data = ...``) need another list.  A captured graph replays what the table names at the time: `set_grads` between replays is seen, and
-    is itself not for capture."""
+    """A planned list of tensors: gradients read and parameters written where they lie, with fp32 state (``state`` tiled,
+    or ``master``/``m``/``v``), 8-bit state (``state8``) or none (norm only). Every argument is a list with one
+    contiguous GPU tensor per list entry; ``grads`` and ``params`` may hold views at any element offset, and a
+    gradient may be None (no gradient in this step: that tensor is left as it is, though the step counts for its
+    bias correction, which has one count for the whole list). Calls run on the current stream of the tensors'
+    device unless a stream is given. The list keeps the tensors, its table and the norm's workspace alive: keep it
+    until its calls are done, and give calls that may overlap in time lists of their own. It names the memory that
+    the tensors had when it was made: parameters that get other memory (``p.data = ...``) need another list. A
+    captured graph replays what the table names at the time: `set_grads` between replays is seen, and is itself not
+    for capture."""
 
     def __init__(self, numels, grads=None, params=None, *, state=None, state8=None, master=None, m=None, v=None,
                  groups=None, n_groups: int = 1):
@@ -388,7 +389,7 @@ class TensorList:
     def _call(self, fn, *args, stream=None) -> None:
         if stream is None:
             stream = _current_raw_stream(self.device.index)
-        elif not isinstance(stream, int) and stream.device != self.device:
+        elif not isinstance(stream, int) and getattr(stream, "device", self.device) != self.device:
             raise ValueError(f"a stream of {stream.device} for a list on {self.device}")
         if torch.cuda.current_device() == self.device.index:
             fn(*args, stream)
@@ -398,9 +399,10 @@ class TensorList:
 
     def _here(self, a, b) -> None:
         at = self.device.index
-        if not ((isinstance(a, int) or a.get_device() == at) and (isinstance(b, int) or b.get_device() == at)):
-            raise ValueError(f"buffers on {' and '.join(str(t.device) for t in (a, b) if not isinstance(t, int))} for "
-                             f"a list on {self.device}")
+        if (isinstance(a, _ADDRESS) or a.get_device() == at) and (isinstance(b, _ADDRESS) or b.get_device() == at):
+            return
+        raise ValueError(f"buffers on {' and '.join(str(t.device) for t in (a, b) if not isinstance(t, _ADDRESS))} for a "
+                         f"list on {self.device}")
 
     def grad_sqnorm(self, sqnorm_out, nonfinite_out, stream=None) -> None:
         """fp64 sum of squares and inf/NaN flag over every gradient."""
@@ -471,7 +473,7 @@ class ListDecision:
             norms = [c.max_norm for c in self.cfgs]
             if norms != self._seen_norms:
                 if len(set(norms)) != 1:
-                    raise ValueError(f"the groups' configurations differ in max_norm ({norms}): give one as an argument")
+                    raise ValueError(f"the configurations differ in max_norm ({norms}): give one as an argument")
                 self.max_norm, self._seen_norms = norms[0], norms
         for k, c in enumerate(self.cfgs):
             now = (c.lr, c.beta1, c.beta2, c.eps, c.weight_decay)

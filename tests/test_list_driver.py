@@ -63,11 +63,10 @@ class HostTorch:
                 return Table.of(self, log)
         return torch.frombuffer(buffer, **kw).as_subclass(Staged)
 
-    def empty(self, *size, device=None, **kw):
-        return torch.empty(*size, **kw)
-
     def zeros(self, n, dtype=torch.float32, device=None):
         return OnGpu(n, dtype, device)
+
+    empty = zeros
 
 
 class Table:
@@ -304,3 +303,17 @@ def test_steps_need_a_list_that_the_update_takes(queued):
     for lst in (whole(sizes), D.TensorList([], []), D.TensorList(sizes, e(sizes), e(sizes), state8=[
             OnGpu(Z.zero_state8_bytes(n), torch.uint8) for n in sizes])):
         D.ListDecision(lst, [D.AdamWConfig()]).step()
+
+
+def test_missing_buffers_and_other_libraries_streams(host, queued, monkeypatch):
+    """A missing output is the library's refusal, and a stream may be any object with a handle."""
+    lst = whole([8, 5000])
+    lst.grad_sqnorm(OnGpu(1, torch.float64), OnGpu(1, torch.int32), types.SimpleNamespace(cuda_stream=0))
+    assert queued == [("norm",)]
+    monkeypatch.setattr(D, "zero_list_grad_sqnorm", Z.zero_list_grad_sqnorm)
+    monkeypatch.setattr(D, "zero_list_adamw_step_dev", Z.zero_list_adamw_step_dev)
+    for call in (lambda: lst.grad_sqnorm(None, OnGpu(1, torch.int32), 0),
+                 lambda: lst.grad_sqnorm(OnGpu(1, torch.float64), None, 0),
+                 lambda: lst.adamw_dev(None, OnGpu(12), 0), lambda: lst.adamw_dev(OnGpu(32), None, 0)):
+        with pytest.raises(Z.ZeroError):
+            call()
