@@ -303,8 +303,8 @@ class BucketPipeline:
 
 
 class TensorList:
-    """A planned list of tensors: gradients read and parameters written where they lie, with fp32 state (``state`` tiled,
-    or ``master``/``m``/``v``), 8-bit state (``state8``) or none (norm only). Every argument is a list with one
+    """A planned list of tensors: gradients read and parameters written where they lie, with fp32 state (``state``
+    tiled, or ``master``/``m``/``v``), 8-bit state (``state8``) or none (norm only). Every argument is a list with one
     contiguous GPU tensor per list entry; ``grads`` and ``params`` may hold views at any element offset, and a
     gradient may be None (no gradient in this step: that tensor is left as it is, though the step counts for its
     bias correction, which has one count for the whole list). Calls run on the current stream of the tensors'
@@ -401,8 +401,8 @@ class TensorList:
         at = self.device.index
         if (isinstance(a, _ADDRESS) or a.get_device() == at) and (isinstance(b, _ADDRESS) or b.get_device() == at):
             return
-        raise ValueError(f"buffers on {' and '.join(str(t.device) for t in (a, b) if not isinstance(t, _ADDRESS))} for a "
-                         f"list on {self.device}")
+        devices = " and ".join(str(t.device) for t in (a, b) if not isinstance(t, _ADDRESS))
+        raise ValueError(f"buffers on {devices} for a list on {self.device}")
 
     def grad_sqnorm(self, sqnorm_out, nonfinite_out, stream=None) -> None:
         """fp64 sum of squares and inf/NaN flag over every gradient."""
@@ -429,13 +429,14 @@ class TensorList:
             raise ValueError(f"lists on {self.device} and {other.device}: a conversion runs on one GPU")
 
     def pack8(self, target: "TensorList", stream=None) -> None:
-        """This list's fp32 state into the 8-bit state of `target` (a list of the same sizes on the same GPU); of
-        master, m and v, one that this list does not have becomes zeros there."""
+        """This list's fp32 state into the 8-bit state of `target` (a list of the same sizes on the same GPU, its
+        state in memory of its own); of master, m and v, one that this list does not have becomes zeros there."""
         self._same_device(target)
         self._call(zero_list_state8_pack, self.list, target.list, stream=stream)
 
     def unpack8(self, target: "TensorList", stream=None) -> None:
-        """This list's 8-bit state into the fp32 state of `target`: those of master, m and v that it has."""
+        """This list's 8-bit state into the fp32 state of `target` (in memory of its own): those of master, m and v
+        that it has."""
         self._same_device(target)
         self._call(zero_list_state8_unpack, self.list, target.list, stream=stream)
 
