@@ -576,6 +576,94 @@ int zero_list_adamw8_step_dev(const zero_list* list, const zero_step_state* stat
 int zero_list_state8_pack(const zero_list* from32, const zero_list* to8, void* stream);
 int zero_list_state8_unpack(const zero_list* from8, const zero_list* to32, void* stream);
 
+/* ------------------------------------------------------------------ the ends of a model
+ *
+ * Where the gradients come from that the step above takes, at the two ends of
+ * a language model and at its norms: the token embedding with its table's
+ * gradient, layer norm with its backward pass, and the softmax cross entropy
+ * of the output head, whose gradients carry the loss scale that
+ * zero_step_state holds on the device.  Weight gradients are written where
+ * the flatten or a list of tensors reads them, in a format of their own,
+ * replacing what is there or added to it (a table that is also the head; the
+ * micro-batches of one step).
+ *
+ *   zero_embed_forward        rows of a table for tokens, scaled
+ *   zero_embed_grad           the table's gradient, by sorted tokens
+ *   zero_layernorm_forward    layer norm, with or without the mean
+ *   zero_layernorm_grad       its three gradients
+ *   zero_loss_head            losses of the head, without keeping its scores
+ *   zero_loss_head_grad       the same, and both gradients
+ *
+ * Sums and statistics are held in fp32; each result is rounded once to its
+ * format, and every sum has one order: the same arguments give the same bits.
+ * Calls are made with the device that holds the buffers current.  A workspace
+ * belongs to one call at a time; what it holds between calls is of no
+ * meaning, so it needs no initial value. */
+
+/* Rows in device memory: row r begins at element r·stride of data.  cols >= 1,
+ * rows and cols at most 2^31 - 1, stride >= cols, rows·stride <= 2^40.  data
+ * is aligned to its elements (no more is needed; rows of whole 16-byte lines
+ * are fastest) and may be NULL where rows = 0. */
+typedef struct zero_rows {
+  void* data;
+  int64_t rows;
+  int64_t cols;
+  int64_t stride;
+  zero_dtype dt;    /* ZERO_BF16, ZERO_FP16 or ZERO_FP32 */
+  int32_t reserved; /* 0 */
+} zero_rows;
+
+/* Device.  out[t] = scale · table[ids[t] - first_row], rounded to out's
+ * format, for out->rows tokens; zeros where that row is not one of the
+ * table's (a rank that holds a slice of the vocabulary adds up the slices'
+ * outputs).  id_bytes: 4 (int32) or 8 (int64).  table and out: any formats,
+ * the same cols. */
+int zero_embed_forward(const zero_rows* table, int64_t first_row, const void* ids_dev, int32_t id_bytes, double scale,
+                       const zero_rows* out, void* stream);
+
+/* Bytes of zero_embed_grad's workspace (16-byte aligned) for up to n_tokens
+ * tokens and a table of table_rows rows of cols elements; 0 if a size is out
+ * of range. */
+size_t zero_embed_grad_workspace_bytes(int64_t n_tokens, int64_t table_rows, int64_t cols);
+
+/* Device.  table_grad[v] = scale · (sum of out_grad[t] over the tokens t with
+ * ids[t] - first_row = v), in fp32 and in an order that only the tokens
+ * decide, rounded once; rows that no token names become zeros.  With
+ * accumulate the sum is added to what table_grad holds, in fp32, and rows
+ * that no token names are not touched.  Tokens outside the table are passed
+ * over, with their out_grad unread. */
+int zero_embed_grad(const void* ids_dev, int32_t id_bytes, int64_t first_row, const zero_rows* out_grad, double scale,
+                    const zero_rows* table_grad, int32_t accumulate, void* ws_dev, size_t ws_bytes, void* stream);
+
+/* Device.  Layer norm of each row of x:
+ *   center = 1:  y = (x - mean)·rstd·weight + bias,  rstd = 1/sqrt(mean((x - mean)²) + eps)
+ *   center = 0:  y = x·rstd·weight + bias,           rstd = 1/sqrt(mean(x²) + eps)
+ * weight_dev and bias_dev (NULL: none): cols elements of format wdt, which is
+ * x's or ZERO_FP32.  y: x's shape and format.  mean_dev, rstd_dev: fp32 per
+ * row, for the backward pass; either may be NULL (mean_dev is not written
+ * where center = 0).  eps >= 0.  cols at most ZERO_LAYERNORM_MAX_COLS (a row
+ * stays in registers between its statistics and its result). */
+#define ZERO_LAYERNORM_MAX_COLS 16384
+int zero_layernorm_forward(const zero_rows* x, const void* weight_dev, const void* bias_dev, zero_dtype wdt, double eps,
+                           int32_t center, const zero_rows* y, float* mean_dev, float* rstd_dev, void* stream);
+
+/* Bytes of zero_layernorm_grad's workspace (16-byte aligned) for up to n_rows
+ * rows of cols elements; 0 if a size is out of range. */
+size_t zero_layernorm_grad_workspace_bytes(int64_t n_rows, int64_t cols);
+
+/* Device.  With h = (x - mean)·rstd and d = y_grad·weight:
+ *   x_grad      = rstd·(d - mean(d) - h·mean(d·h))     (without mean(d) where center = 0)
+ *   weight_grad = sum of y_grad·h over the rows
+ *   bias_grad   = sum of y_grad over the rows
+ * mean_dev and rstd_dev as the forward pass left them (mean_dev is not read
+ * where center = 0).  y_grad and x_grad: x's shape and format.  weight_grad
+ * and bias_grad: cols elements of format gdt (any), added to what they hold
+ * with accumulate.  Each of the three results may be left out (NULL). */
+int zero_layernorm_grad(const zero_rows* x, const zero_rows* y_grad, const void* weight_dev, zero_dtype wdt,
+                        int32_t center, const float* mean_dev, const float* rstd_dev, const zero_rows* x_grad,
+                        void* weight_grad_dev, void* bias_grad_dev, zero_dtype gdt, int32_t accumulate, void* ws_dev,
+                        size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ measurement aid
  *
  * Not a step of the method: the read-modify-write ceiling of the tiled

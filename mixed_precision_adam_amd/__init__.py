@@ -2,8 +2,7 @@
 
 Argument marshalling only.  Every function has the name of the C entry point
 it wraps (declared in include/zero_shard.h); all device work runs in the HIP
-kernels of ``csrc/zero_shard.hip`` and ``csrc/zero_list.hip``.  PyTorch supplies device memory and the
-stream.  There is no fallback: if the library is missing, importing this
+kernels of ``csrc/*.hip``.  PyTorch supplies device memory and the stream.  There is no fallback: if the library is missing, importing this
 package raises.
 """
 from __future__ import annotations
@@ -158,6 +157,24 @@ _lib.zero_list_adamw8_step_dev.argtypes = [_LIST, _P, _P, C.c_uint64, _P]
 _lib.zero_list_state8_pack.argtypes = [_LIST, _LIST, _P]
 _lib.zero_list_state8_unpack.argtypes = [_LIST, _LIST, _P]
 
+
+
+class zero_rows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64), ("stride", C.c_int64),
+                ("dt", C.c_int32), ("reserved", C.c_int32)]
+
+
+_ROWS = C.POINTER(zero_rows)
+_lib.zero_embed_forward.argtypes = [_ROWS, C.c_int64, _P, C.c_int32, C.c_double, _ROWS, _P]
+_lib.zero_embed_grad_workspace_bytes.argtypes = [C.c_int64, C.c_int64, C.c_int64]
+_lib.zero_embed_grad_workspace_bytes.restype = C.c_size_t
+_lib.zero_embed_grad.argtypes = [_P, C.c_int32, C.c_int64, _ROWS, C.c_double, _ROWS, C.c_int32, _P, C.c_size_t, _P]
+_lib.zero_layernorm_forward.argtypes = [_ROWS, _P, _P, C.c_int32, C.c_double, C.c_int32, _ROWS, _P, _P, _P]
+_lib.zero_layernorm_grad_workspace_bytes.argtypes = [C.c_int64, C.c_int64]
+_lib.zero_layernorm_grad_workspace_bytes.restype = C.c_size_t
+_lib.zero_layernorm_grad.argtypes = [_ROWS, _ROWS, _P, C.c_int32, C.c_int32, _P, _P, _ROWS, _P, _P, C.c_int32,
+                                     C.c_int32, _P, C.c_size_t, _P]
+
 # Every symbol include/zero_shard.h declares.
 EXPORTS = ("zero_last_error", "zero_shard_layout", "zero_flatten_plan", "zero_bucket_segments", "zero_flatten_grads",
            "zero_flatten_grads_sqnorm", "zero_flatten_partials_count", "zero_flatten_grads_partials",
@@ -169,7 +186,8 @@ EXPORTS = ("zero_last_error", "zero_shard_layout", "zero_flatten_plan", "zero_bu
            "zero_list_table_bytes", "zero_list_plan", "zero_list_repoint", "zero_list_grad_sqnorm_workspace_bytes",
            "zero_list_grad_sqnorm", "zero_list_adamw_step", "zero_list_adamw8_step", "zero_list_decision_dev",
            "zero_list_adamw_step_dev", "zero_list_adamw8_step_dev", "zero_list_state8_pack",
-           "zero_list_state8_unpack")
+           "zero_list_state8_unpack", "zero_embed_forward", "zero_embed_grad_workspace_bytes", "zero_embed_grad",
+           "zero_layernorm_forward", "zero_layernorm_grad_workspace_bytes", "zero_layernorm_grad")
 ZERO_STEP_ERR_LOSS_SCALE = 1  # zero_step_state.error: the decision could not be taken
 ZERO_NOALLOC_SCRATCH_BYTES = 6 << 20  # static scratch of zero_flatten_grads_sqnorm_noalloc, per device
 
@@ -532,6 +550,103 @@ def zero_list_state8_pack(from32: zero_list, to8: zero_list, stream=None) -> Non
 
 def zero_list_state8_unpack(from8: zero_list, to32: zero_list, stream=None) -> None:
     _check(_lib.zero_list_state8_unpack(C.byref(from8), C.byref(to32), _stream(stream)))
+
+
+# ---------------------------------------------------------------------- the ends of a model
+
+ZERO_LAYERNORM_MAX_COLS = 16384
+_FORMAT = {torch.bfloat16: ZERO_BF16, torch.float16: ZERO_FP16, torch.float32: ZERO_FP32}
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _rows(x, name: str = "rows") -> zero_rows:
+    """The zero_rows of a 2-D tensor whose rows are contiguous (a zero_rows is taken as it is)."""
+    if isinstance(x, zero_rows):
+        return x
+    if not x.is_cuda:
+        raise ValueError(f"{name}: a GPU tensor is required, got one on {x.device}")
+    if x.dim() != 2 or x.dtype not in _FORMAT:
+        raise ValueError(f"{name}: a matrix in bf16, fp16 or fp32 is required, got {x.dtype} {tuple(x.shape)}")
+    rows, cols = x.shape
+    stride, step = x.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name}: rows must be contiguous, got strides {tuple(x.stride())}")
+    if rows <= 1:
+        stride = cols
+    elif stride < cols:
+        raise ValueError(f"{name}: rows overlap, strides {tuple(x.stride())}")
+    return zero_rows(x.data_ptr(), rows, cols, stride, _FORMAT[x.dtype], 0)
+
+
+def _ids(x, n: int):
+    """(address, bytes of one) of n contiguous int32 or int64."""
+    if x.dtype not in _ID_BYTES:
+        raise ValueError(f"int32 or int64 is required, got {x.dtype}")
+    if x.numel() != n:
+        raise ValueError(f"{x.numel()} tokens for {n} rows")
+    return _addr(x), _ID_BYTES[x.dtype]
+
+
+def _vector(x, n: int, name: str, formats=_FORMAT):
+    """(address, format) of n contiguous elements, or (None, None)."""
+    if x is None:
+        return None, None
+    if x.dtype not in formats:
+        raise ValueError(f"{name}: dtype {x.dtype} where one of {sorted(map(str, formats))} is needed")
+    if x.numel() != n:
+        raise ValueError(f"{name}: {x.numel()} elements where {n} are needed")
+    return _addr(x), _FORMAT[x.dtype]
+
+
+_FP32_ONLY = {torch.float32: ZERO_FP32}
+
+
+def zero_embed_forward(table, ids, out, *, scale: float = 1.0, first_row: int = 0, stream=None) -> None:
+    table, out = _rows(table, "table"), _rows(out, "out")
+    _check(_lib.zero_embed_forward(table, first_row, *_ids(ids, out.rows), scale, out, _stream(stream)))
+
+
+def zero_embed_grad_workspace_bytes(n_tokens: int, table_rows: int, cols: int) -> int:
+    return int(_lib.zero_embed_grad_workspace_bytes(n_tokens, table_rows, cols))
+
+
+def zero_embed_grad(ids, out_grad, table_grad, ws, ws_bytes: int, *, scale: float = 1.0, first_row: int = 0,
+                    accumulate: bool = False, stream=None) -> None:
+    out_grad, table_grad = _rows(out_grad, "out_grad"), _rows(table_grad, "table_grad")
+    _check(_lib.zero_embed_grad(*_ids(ids, out_grad.rows), first_row, out_grad, scale, table_grad, int(accumulate),
+                                _buf(ws, ws_bytes), ws_bytes, _stream(stream)))
+
+
+def zero_layernorm_forward(x, weight, bias, y, mean, rstd, *, eps: float = 1e-5, center: bool = True,
+                           stream=None) -> None:
+    x, y = _rows(x, "x"), _rows(y, "y")
+    w, wdt = _vector(weight, x.cols, "weight")
+    b, bdt = _vector(bias, x.cols, "bias")
+    if b is not None and bdt != wdt:
+        raise ValueError("weight and bias differ in dtype")
+    _check(_lib.zero_layernorm_forward(x, w, b, -1 if wdt is None else wdt, eps, int(center), y,
+                                       _vector(mean, x.rows, "mean", _FP32_ONLY)[0],
+                                       _vector(rstd, x.rows, "rstd", _FP32_ONLY)[0], _stream(stream)))
+
+
+def zero_layernorm_grad_workspace_bytes(n_rows: int, cols: int) -> int:
+    return int(_lib.zero_layernorm_grad_workspace_bytes(n_rows, cols))
+
+
+def zero_layernorm_grad(x, y_grad, weight, mean, rstd, x_grad, weight_grad, bias_grad, ws, ws_bytes: int, *,
+                        center: bool = True, accumulate: bool = False, stream=None) -> None:
+    x, y_grad = _rows(x, "x"), _rows(y_grad, "y_grad")
+    x_grad = None if x_grad is None else _rows(x_grad, "x_grad")
+    w, wdt = _vector(weight, x.cols, "weight")
+    dw, gdt = _vector(weight_grad, x.cols, "weight_grad")
+    db, bdt = _vector(bias_grad, x.cols, "bias_grad")
+    if dw is not None and db is not None and gdt != bdt:
+        raise ValueError("weight_grad and bias_grad differ in dtype")
+    gdt = ZERO_FP32 if gdt is None and bdt is None else bdt if gdt is None else gdt
+    _check(_lib.zero_layernorm_grad(x, y_grad, w, -1 if wdt is None else wdt, int(center),
+                                    _vector(mean, x.rows, "mean", _FP32_ONLY)[0],
+                                    _vector(rstd, x.rows, "rstd", _FP32_ONLY)[0], x_grad, dw, db, gdt,
+                                    int(accumulate), _buf(ws, ws_bytes), ws_bytes, _stream(stream)))
 
 
 def read_step_state(state_tensor) -> dict:

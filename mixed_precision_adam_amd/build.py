@@ -6,6 +6,7 @@ the library, and a second HIP runtime in the same process would not see them.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 
@@ -13,6 +14,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "zero_shard.hip")
 LIST_SRC = os.path.join(HERE, "csrc", "zero_list.hip")
+EMBED_SRC = os.path.join(HERE, "csrc", "zero_embed.hip")
+NORM_SRC = os.path.join(HERE, "csrc", "zero_norm.hip")
+SOURCES = (SRC, LIST_SRC, EMBED_SRC, NORM_SRC)
 LIB = os.path.join(HERE, "libzero_shard.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CLANG = "/opt/rocm/llvm/bin/clang++"
@@ -60,10 +64,10 @@ def build(verbose: bool = False) -> str:
     """Compile the library (always rebuilds) and return its path."""
     tlib = torch_lib_dir()
     tmp = LIB + ".tmp"
-    objs, log = [], ""
-    for src in (SRC, LIST_SRC):
-        objs.append(f"{LIB}.{os.path.basename(src)}.o")
-        log += _run([HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-c", "-o", objs[-1], src])
+    objs = [f"{LIB}.{os.path.basename(src)}.o" for src in SOURCES]
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as pool:
+        log = "".join(pool.map(lambda src, obj: _run([HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-c", "-o",
+                                                      obj, src]), SOURCES, objs))
     log += _run([CLANG, "-shared", "-o", tmp, *objs, "-L", tlib, "-l:libamdhip64.so", f"-Wl,-rpath,{tlib}",
                  "-Wl,--no-undefined", "-lm"])
     for obj in objs:

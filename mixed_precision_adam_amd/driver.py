@@ -7,8 +7,9 @@ ways of sequencing it: ``rank_step`` (decision on the host after a 16-byte
 readback), ``DeviceDecision`` (decision on the GPU, nothing waits on the
 host) and ``BucketPipeline`` (flatten + norm partials in constant-capacity
 buckets as gradients arrive on a producer stream).  ``TensorList`` and
-``ListDecision`` step many tensors where they lie.  No arithmetic of the
-method happens here: every step is a library call.
+``ListDecision`` step many tensors where they lie.  ``TokenEmbedding`` and
+``LayerNorm`` compute at a model's ends and norms, where the gradients come
+from.  No arithmetic of the method happens here: every step is a library call.
 """
 from __future__ import annotations
 
@@ -20,9 +21,11 @@ import torch
 from . import (ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO_LIST_HAS_PARAMS, ZERO_LIST_WHOLE_STATE, ZERO_STATE_8BIT,
                ZERO_STATE_ARRAYS, ZERO_STATE_NONE, ZERO_STATE_TILE, ZERO_STATE_TILED, _buf, read_step_state,
                zero_adamw_hparams, zero_adamw_step, zero_adamw_step_dev, zero_adamw_step_tiled,
-               zero_adamw_step_tiled_dev, zero_bucket_segments, zero_flatten_grads, zero_flatten_grads_partials,
+               zero_adamw_step_tiled_dev, zero_bucket_segments, zero_embed_forward, zero_embed_grad,
+               zero_embed_grad_workspace_bytes, zero_flatten_grads, zero_flatten_grads_partials,
                zero_flatten_grads_sqnorm, zero_flatten_partials_count, zero_flatten_plan, zero_grad_sqnorm,
-               zero_grad_sqnorm_workspace_bytes, zero_list_adamw8_step, zero_list_adamw8_step_dev,
+               zero_grad_sqnorm_workspace_bytes, zero_layernorm_forward, zero_layernorm_grad,
+               zero_layernorm_grad_workspace_bytes, zero_list_adamw8_step, zero_list_adamw8_step_dev,
                zero_list_adamw_step, zero_list_adamw_step_dev, zero_list_decision_dev, zero_list_grad_sqnorm,
                zero_list_grad_sqnorm_workspace_bytes, zero_list_plan, zero_list_repoint, zero_list_state8_pack,
                zero_list_state8_unpack, zero_list_tensor, zero_shard_layout, zero_sqnorm_reduce, zero_state8_bytes,
@@ -494,6 +497,95 @@ class ListDecision:
         """The decided state of the last step queued, on whatever stream (synchronizes the device)."""
         torch.cuda.synchronize(self.tensors.device)
         return read_step_state(self.state)
+
+
+class _Operator:
+    """An operator over tensors of one GPU: its calls run on the current stream of that GPU unless a stream is given.
+    It keeps its tensors and its workspace alive: keep it until its calls are done, and give calls that may overlap in
+    time (two streams, two captured graphs) operators of their own."""
+
+    def _on(self, *tensors) -> None:
+        at = self.device.index
+        for t in tensors:
+            if t is not None and t.get_device() != at:
+                raise ValueError(f"a tensor on {t.device} for an operator on {self.device}")
+
+    def _call(self, fn, *args, stream=None, **more) -> None:
+        if stream is None:
+            stream = _current_raw_stream(self.device.index)
+        elif not isinstance(stream, int) and getattr(stream, "device", self.device) != self.device:
+            raise ValueError(f"a stream of {stream.device} for an operator on {self.device}")
+        if torch.cuda.current_device() == self.device.index:
+            fn(*args, stream=stream, **more)
+        else:  # kernels are launched from the device that holds the tensors
+            with torch.cuda.device(self.device):
+                fn(*args, stream=stream, **more)
+
+    def _workspace(self, nbytes: int, workspace) -> None:
+        """A workspace of its own, or a part of one that is shared with operators whose calls do not overlap."""
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self._on(workspace)
+        if workspace.dtype != torch.uint8 or workspace.numel() < nbytes:
+            raise ValueError(f"a workspace of {nbytes} bytes (uint8) is needed")
+        self.ws, self.ws_bytes = workspace, nbytes
+
+
+class TokenEmbedding(_Operator):
+    """Rows of `table` for tokens, times `scale`, and the table's gradient.  A rank that holds a slice of the vocabulary
+    names its first row: tokens outside the slice get zeros, and give no gradient.  `max_tokens`: the most that one
+    call of `grad` takes (0: no gradients, no workspace)."""
+
+    def __init__(self, table, *, max_tokens: int = 0, scale: float = 1.0, first_row: int = 0, workspace=None):
+        self.table, self.scale, self.first_row, self.max_tokens = table, float(scale), first_row, max_tokens
+        self.device = table.device
+        if max_tokens:
+            need = zero_embed_grad_workspace_bytes(max_tokens, *table.shape)
+            if need == 0:
+                raise ValueError(f"{max_tokens} tokens over a table of {tuple(table.shape)}: out of range")
+            self._workspace(need, workspace)
+
+    def forward(self, ids, out, stream=None) -> None:
+        """out[t] = scale * table[ids[t] - first_row]."""
+        self._on(ids, out)
+        self._call(zero_embed_forward, self.table, ids, out, scale=self.scale, first_row=self.first_row, stream=stream)
+
+    def grad(self, ids, out_grad, table_grad, accumulate: bool = False, stream=None) -> None:
+        """The table's gradient (any format and row stride), in place of what `table_grad` holds or added to it."""
+        self._on(ids, out_grad, table_grad)
+        if table_grad.shape != self.table.shape:
+            raise ValueError(f"a gradient of {tuple(table_grad.shape)} for a table of {tuple(self.table.shape)}")
+        if out_grad.shape[0] > self.max_tokens:
+            raise ValueError(f"{out_grad.shape[0]} tokens, made for {self.max_tokens} (max_tokens)")
+        self._call(zero_embed_grad, ids, out_grad, table_grad, self.ws, self.ws_bytes, scale=self.scale,
+                   first_row=self.first_row, accumulate=accumulate, stream=stream)
+
+
+class LayerNorm(_Operator):
+    """Layer norm over the rows of a matrix (`mean=False`: without subtracting the mean), and its gradients.  Norms
+    whose calls do not overlap in time may share a workspace (`workspace=other.ws`)."""
+
+    def __init__(self, weight, bias=None, *, eps: float = 1e-5, mean: bool = True, workspace=None):
+        self.weight, self.bias, self.eps, self.mean = weight, bias, float(eps), bool(mean)
+        self.device = weight.device
+        self._on(bias)
+        need = zero_layernorm_grad_workspace_bytes(2**31 - 1, weight.numel())  # enough for any number of rows
+        if need == 0:
+            raise ValueError(f"rows of {weight.numel()} elements: out of range")
+        self._workspace(need, workspace)
+
+    def forward(self, x, out, mean=None, rstd=None, stream=None) -> None:
+        """The statistics of each row are left in `mean` and `rstd` (fp32) where these are given."""
+        self._on(x, out, mean, rstd)
+        self._call(zero_layernorm_forward, x, self.weight, self.bias, out, mean, rstd, eps=self.eps, center=self.mean,
+                   stream=stream)
+
+    def grad(self, x, out_grad, mean, rstd, x_grad=None, weight_grad=None, bias_grad=None, accumulate: bool = False,
+             stream=None) -> None:
+        """Those gradients that are given a place; `accumulate`: the weight's and the bias's are added to theirs."""
+        self._on(x, out_grad, mean, rstd, x_grad, weight_grad, bias_grad)
+        self._call(zero_layernorm_grad, x, out_grad, self.weight, mean, rstd, x_grad, weight_grad, bias_grad, self.ws,
+                   self.ws_bytes, center=self.mean, accumulate=accumulate, stream=stream)
 
 
 def wait_spin(stream) -> None:
