@@ -664,6 +664,41 @@ int zero_layernorm_grad(const zero_rows* x, const zero_rows* y_grad, const void*
                         void* weight_grad_dev, void* bias_grad_dev, zero_dtype gdt, int32_t accumulate, void* ws_dev,
                         size_t ws_bytes, void* stream);
 
+/* Bytes of the workspace (256-byte aligned) of zero_loss_head (gradients = 0)
+ * and zero_loss_head_grad (gradients = 1) for up to n_tokens tokens, whatever
+ * the strides; 0 if a size is out of range.  It does not grow with n_tokens
+ * past some thousands: scores exist for one block of tokens at a time. */
+size_t zero_loss_head_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t cols, int32_t gradients);
+
+/* Device.  Scores z = x·tableᵀ of x->rows tokens over table->rows words, and
+ *   losses[t] = log(sum of exp(z[t])) - z[t][labels[t]]
+ *   *loss     = sum of losses / count,  *count = number of tokens that count
+ * A label outside [0, table->rows) does not count: its loss is 0, its
+ * gradients zeros.  Where none counts, *loss is 0.  x and table: the same
+ * 16-bit format and cols (fp32 is refused: the products take 16-bit factors).
+ * label_bytes: 4 (int32) or 8 (int64).  losses_dev (x->rows), loss_dev: fp32.
+ * Scores are sums in fp32, never rounded to fewer bits for the losses.  A
+ * score that is NaN or +inf makes its token's loss (and gradients) NaN; one of
+ * -inf is a word of probability 0.  table->rows in [1, 2^22], cols at most
+ * 2^16. */
+int zero_loss_head(const zero_rows* x, const zero_rows* table, const void* labels_dev, int32_t label_bytes,
+                   float* losses_dev, float* loss_dev, int64_t* count_dev, void* ws_dev, size_t ws_bytes, void* stream);
+
+/* Device.  The same, and the gradients of *loss times the loss scale:
+ *   G = (softmax(z) - onehot(label))·scale·loss_scale/count   (zeros for tokens that do not count)
+ *   x_grad     = G·table     (x's shape and format)
+ *   table_grad = Gᵀ·x        (table's shape and format), or added to what it
+ *                            holds with accumulate
+ * loss_scale is state_dev->loss_scale when the kernels run (1 where state_dev
+ * is NULL), so a captured step follows the scale that the decision moves.  The
+ * factors softmax - onehot are rounded to the 16-bit format for the products.
+ * A token that does not count has no part in the gradients, whatever its row
+ * of x holds. */
+int zero_loss_head_grad(const zero_rows* x, const zero_rows* table, const void* labels_dev, int32_t label_bytes,
+                        double scale, const zero_step_state* state_dev, float* losses_dev, float* loss_dev,
+                        int64_t* count_dev, const zero_rows* x_grad, const zero_rows* table_grad, int32_t accumulate,
+                        void* ws_dev, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ measurement aid
  *
  * Not a step of the method: the read-modify-write ceiling of the tiled

@@ -2,7 +2,8 @@
 
 Argument marshalling only.  Every function has the name of the C entry point
 it wraps (declared in include/zero_shard.h); all device work runs in the HIP
-kernels of ``csrc/*.hip``.  PyTorch supplies device memory and the stream.  There is no fallback: if the library is missing, importing this
+kernels of ``csrc/*.hip``.  PyTorch supplies device memory and the
+stream.  There is no fallback: if the library is missing, importing this
 package raises.
 """
 from __future__ import annotations
@@ -174,6 +175,11 @@ _lib.zero_layernorm_grad_workspace_bytes.argtypes = [C.c_int64, C.c_int64]
 _lib.zero_layernorm_grad_workspace_bytes.restype = C.c_size_t
 _lib.zero_layernorm_grad.argtypes = [_ROWS, _ROWS, _P, C.c_int32, C.c_int32, _P, _P, _ROWS, _P, _P, C.c_int32,
                                      C.c_int32, _P, C.c_size_t, _P]
+_lib.zero_loss_head_workspace_bytes.argtypes = [C.c_int64, C.c_int64, C.c_int64, C.c_int32]
+_lib.zero_loss_head_workspace_bytes.restype = C.c_size_t
+_lib.zero_loss_head.argtypes = [_ROWS, _ROWS, _P, C.c_int32, _P, _P, _P, _P, C.c_size_t, _P]
+_lib.zero_loss_head_grad.argtypes = [_ROWS, _ROWS, _P, C.c_int32, C.c_double, _P, _P, _P, _P, _ROWS, _ROWS, C.c_int32,
+                                     _P, C.c_size_t, _P]
 
 # Every symbol include/zero_shard.h declares.
 EXPORTS = ("zero_last_error", "zero_shard_layout", "zero_flatten_plan", "zero_bucket_segments", "zero_flatten_grads",
@@ -187,7 +193,8 @@ EXPORTS = ("zero_last_error", "zero_shard_layout", "zero_flatten_plan", "zero_bu
            "zero_list_grad_sqnorm", "zero_list_adamw_step", "zero_list_adamw8_step", "zero_list_decision_dev",
            "zero_list_adamw_step_dev", "zero_list_adamw8_step_dev", "zero_list_state8_pack",
            "zero_list_state8_unpack", "zero_embed_forward", "zero_embed_grad_workspace_bytes", "zero_embed_grad",
-           "zero_layernorm_forward", "zero_layernorm_grad_workspace_bytes", "zero_layernorm_grad")
+           "zero_layernorm_forward", "zero_layernorm_grad_workspace_bytes", "zero_layernorm_grad",
+           "zero_loss_head_workspace_bytes", "zero_loss_head", "zero_loss_head_grad")
 ZERO_STEP_ERR_LOSS_SCALE = 1  # zero_step_state.error: the decision could not be taken
 ZERO_NOALLOC_SCRATCH_BYTES = 6 << 20  # static scratch of zero_flatten_grads_sqnorm_noalloc, per device
 
@@ -647,6 +654,34 @@ def zero_layernorm_grad(x, y_grad, weight, mean, rstd, x_grad, weight_grad, bias
                                     _vector(mean, x.rows, "mean", _FP32_ONLY)[0],
                                     _vector(rstd, x.rows, "rstd", _FP32_ONLY)[0], x_grad, dw, db, gdt,
                                     int(accumulate), _buf(ws, ws_bytes), ws_bytes, _stream(stream)))
+
+
+def zero_loss_head_workspace_bytes(n_tokens: int, vocab: int, cols: int, gradients: bool = True) -> int:
+    return int(_lib.zero_loss_head_workspace_bytes(n_tokens, vocab, cols, int(gradients)))
+
+
+def _scalar(x, dtype, name: str):
+    """Address of one value on the device."""
+    if x.dtype != dtype or x.numel() != 1:
+        raise ValueError(f"{name}: one value of {dtype} is needed, got {x.numel()} of {x.dtype}")
+    return _addr(x)
+
+
+def zero_loss_head(x, table, labels, losses, loss, count, ws, ws_bytes: int, *, stream=None) -> None:
+    x, table = _rows(x, "x"), _rows(table, "table")
+    _check(_lib.zero_loss_head(x, table, *_ids(labels, x.rows), _vector(losses, x.rows, "losses", _FP32_ONLY)[0],
+                               _scalar(loss, torch.float32, "loss"), _scalar(count, torch.int64, "count"),
+                               _buf(ws, ws_bytes), ws_bytes, _stream(stream)))
+
+
+def zero_loss_head_grad(x, table, labels, losses, loss, count, x_grad, table_grad, ws, ws_bytes: int, *,
+                        scale: float = 1.0, accumulate: bool = False, step_state=None, stream=None) -> None:
+    x, table = _rows(x, "x"), _rows(table, "table")
+    _check(_lib.zero_loss_head_grad(x, table, *_ids(labels, x.rows), scale, _buf(step_state, _STATE),
+                                    _vector(losses, x.rows, "losses", _FP32_ONLY)[0],
+                                    _scalar(loss, torch.float32, "loss"), _scalar(count, torch.int64, "count"),
+                                    _rows(x_grad, "x_grad"), _rows(table_grad, "table_grad"), int(accumulate),
+                                    _buf(ws, ws_bytes), ws_bytes, _stream(stream)))
 
 
 def read_step_state(state_tensor) -> dict:

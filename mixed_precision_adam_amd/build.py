@@ -16,7 +16,8 @@ SRC = os.path.join(HERE, "csrc", "zero_shard.hip")
 LIST_SRC = os.path.join(HERE, "csrc", "zero_list.hip")
 EMBED_SRC = os.path.join(HERE, "csrc", "zero_embed.hip")
 NORM_SRC = os.path.join(HERE, "csrc", "zero_norm.hip")
-SOURCES = (SRC, LIST_SRC, EMBED_SRC, NORM_SRC)
+HEAD_SRC = os.path.join(HERE, "csrc", "zero_head.hip")
+SOURCES = (SRC, LIST_SRC, EMBED_SRC, NORM_SRC, HEAD_SRC)
 LIB = os.path.join(HERE, "libzero_shard.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CLANG = "/opt/rocm/llvm/bin/clang++"

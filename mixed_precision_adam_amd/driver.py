@@ -7,9 +7,9 @@ ways of sequencing it: ``rank_step`` (decision on the host after a 16-byte
 readback), ``DeviceDecision`` (decision on the GPU, nothing waits on the
 host) and ``BucketPipeline`` (flatten + norm partials in constant-capacity
 buckets as gradients arrive on a producer stream).  ``TensorList`` and
-``ListDecision`` step many tensors where they lie.  ``TokenEmbedding`` and
-``LayerNorm`` compute at a model's ends and norms, where the gradients come
-from.  No arithmetic of the method happens here: every step is a library call.
+``ListDecision`` step many tensors where they lie.  ``TokenEmbedding``,
+``LayerNorm`` and ``LossHead`` compute at a model's ends and norms, where the
+gradients come from.  No arithmetic of the method happens here: every step is a library call.
 """
 from __future__ import annotations
 
@@ -28,7 +28,8 @@ from . import (ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO_LIST_HAS_PARAMS, ZERO_LIST_
                zero_layernorm_grad_workspace_bytes, zero_list_adamw8_step, zero_list_adamw8_step_dev,
                zero_list_adamw_step, zero_list_adamw_step_dev, zero_list_decision_dev, zero_list_grad_sqnorm,
                zero_list_grad_sqnorm_workspace_bytes, zero_list_plan, zero_list_repoint, zero_list_state8_pack,
-               zero_list_state8_unpack, zero_list_tensor, zero_shard_layout, zero_sqnorm_reduce, zero_state8_bytes,
+               zero_list_state8_unpack, zero_list_tensor, zero_loss_head, zero_loss_head_grad,
+               zero_loss_head_workspace_bytes, zero_shard_layout, zero_sqnorm_reduce, zero_state8_bytes,
                zero_state_tile, zero_state_tiled_numel, zero_state_untile, zero_step_decision, zero_step_decision_dev,
                zero_step_state_init)
 
@@ -586,6 +587,41 @@ class LayerNorm(_Operator):
         self._on(x, out_grad, mean, rstd, x_grad, weight_grad, bias_grad)
         self._call(zero_layernorm_grad, x, out_grad, self.weight, mean, rstd, x_grad, weight_grad, bias_grad, self.ws,
                    self.ws_bytes, center=self.mean, accumulate=accumulate, stream=stream)
+
+
+class LossHead(_Operator):
+    """Softmax cross entropy of the linear head `table` (words x columns, 16-bit) over hidden rows, without keeping the
+    scores, and its gradients.  Labels outside the vocabulary do not count.  `max_tokens`: the most that one call
+    takes; `gradients=False`: a smaller workspace, for losses alone."""
+
+    def __init__(self, table, *, max_tokens: int, gradients: bool = True, workspace=None):
+        self.table, self.max_tokens, self.gradients = table, max_tokens, bool(gradients)
+        self.device = table.device
+        need = zero_loss_head_workspace_bytes(max_tokens, *table.shape, gradients)
+        if need == 0:
+            raise ValueError(f"{max_tokens} tokens over a table of {tuple(table.shape)}: out of range")
+        self._workspace(need, workspace)
+
+    def _fits(self, x) -> None:
+        if x.shape[0] > self.max_tokens:
+            raise ValueError(f"{x.shape[0]} tokens, made for {self.max_tokens} (max_tokens)")
+
+    def forward(self, x, labels, losses, loss, count, stream=None) -> None:
+        """losses[t] (fp32; 0 where the label does not count), their mean in `loss` (fp32) and how many count (int64)."""
+        self._on(x, labels, losses, loss, count)
+        self._fits(x)
+        self._call(zero_loss_head, x, self.table, labels, losses, loss, count, self.ws, self.ws_bytes, stream=stream)
+
+    def grad(self, x, labels, losses, loss, count, x_grad, table_grad, accumulate: bool = False, step_state=None,
+             scale: float = 1.0, stream=None) -> None:
+        """The same, and the gradients of `loss` times `scale` and the loss scale in `step_state` (ListDecision.state,
+        DeviceDecision.state; None: 1); `accumulate`: the table's is added to what `table_grad` holds."""
+        if not self.gradients:
+            raise ValueError("made without gradients")
+        self._on(x, labels, losses, loss, count, x_grad, table_grad, step_state)
+        self._fits(x)
+        self._call(zero_loss_head_grad, x, self.table, labels, losses, loss, count, x_grad, table_grad, self.ws,
+                   self.ws_bytes, scale=scale, accumulate=accumulate, step_state=step_state, stream=stream)
 
 
 def wait_spin(stream) -> None:

@@ -1,0 +1,216 @@
+"""The loss head (softmax cross entropy over a large vocabulary) against a plain implementation in 64 bits, on the GPU.
+
+Tolerances.  A score is a sum of d products in fp32: off by at most d * 2^-24 of the sum of their magnitudes, S.  Losses
+are two such scores apart and add a handful of roundings of the largest.  A factor of the gradients' products (softmax -
+onehot) comes from a score held to 2^-12 of an octave and is rounded once to 16 bits: off by e = 2^-12 ln 2 + eps / 2
+of itself, and by what the scores are off; a word further than 32 octaves below its piece's maximum counts as 0."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_ends import DEV, U, between, check, half_step, matrix
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import mixed_precision_adam_amd as Z
+    from mixed_precision_adam_amd.driver import LossHead
+
+FORMATS = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+class Head:
+    """Inputs of one call, its outputs (with what lies between their rows), and the results in 64 bits."""
+
+    def __init__(self, tokens, vocab, cols, dt, spare=0, shift=0, ignored=0.2, seed=0, sigma=0.05, sure=0.0):
+        gen = torch.Generator(DEV).manual_seed(tokens * 7 + vocab * 3 + cols + seed)
+        self.dtype = FORMATS[dt]
+        self.table, _ = matrix(vocab, cols, self.dtype, gen, sigma, spare, shift)
+        self.labels = torch.randint(0, vocab, (tokens,), generator=gen, device=DEV)
+        self.x, _ = matrix(tokens, cols, self.dtype, gen, 1.0, spare, shift)
+        if sure:
+            self.x.add_((self.table[self.labels].float() * (sure / (sigma * sigma * cols))).to(self.dtype))
+        self.labels[torch.rand(tokens, generator=gen, device=DEV) < ignored] = -100
+        self.losses = torch.full((tokens,), 9.0, device=DEV)
+        self.loss, self.count = torch.full((1,), 9.0, device=DEV), torch.full((1,), 9, device=DEV)
+        self.dx, self.dx_buf = matrix(tokens, cols, self.dtype, gen, 1.0, spare, shift)
+        self.dw, self.dw_buf = matrix(vocab, cols, self.dtype, gen, 0.01, spare, shift)
+        self.old = self.dw.clone()
+        self.rest = between(self.dx, self.dx_buf), between(self.dw, self.dw_buf)
+        self.vocab, self.cols = vocab, cols
+
+    def want(self, scale=1.0):
+        x, w = self.x.double(), self.table.double()
+        counts = (self.labels >= 0) & (self.labels < self.vocab)
+        x = torch.where(counts[:, None], x, 0.0)
+        label = self.labels.clamp(0, self.vocab - 1)[:, None]
+        z = x @ w.t()
+        slack_z = self.cols * U * (x.abs() @ w.abs().t())  # of each score
+        lse = torch.logsumexp(z, 1, keepdim=True)
+        slack = slack_z.amax(1, keepdim=True) + 16 * U * (1 + z.abs().amax(1, keepdim=True))
+        self.counts = counts
+        self.want_losses = torch.where(counts, (lse - z.gather(1, label))[:, 0], 0.0)
+        self.slack_losses = 2 * slack[:, 0]
+        n = max(1, int(counts.sum()))
+        factor = scale / n
+        p = (z - lse).exp()
+        g = p.scatter_add(1, label, torch.full_like(lse, -1.0))
+        g.scatter_(1, label, torch.expm1(-self.want_losses)[:, None])
+        fmt = torch.finfo(self.dtype)
+        least = fmt.tiny * fmt.eps / (2 if self.dtype == torch.bfloat16 else 2.0**16)  # half the least step of a factor
+        e = g.abs() * (2.0**-12 * math.log(2) + fmt.eps / 2) + (p + g.abs()) * 2 * slack + 2.0**-31 + least
+        g, e = g * counts[:, None], e * counts[:, None]
+        self.want_dx, self.slack_dx = (g @ w) * factor, (e @ w.abs()) * factor
+        self.slack_dx += 2.0**-14 * self.slack_dx + self.vocab * U * (g.abs() @ w.abs()) * factor
+        self.want_dw, self.slack_dw = (g.t() @ x) * factor, (e.t() @ x.abs()) * factor
+        self.slack_dw += len(x) * U * (g.abs().t() @ x.abs()) * factor
+        return self
+
+    def check_losses(self):
+        check("losses", self.losses, self.want_losses, self.slack_losses + U * self.want_losses.abs())
+        n = int(self.counts.sum())
+        assert self.count.item() == n
+        check("loss", self.loss, self.want_losses.sum().view(1) / max(1, n),
+              self.slack_losses.max().view(1) + U * self.want_losses.abs().max() if n else torch.zeros(1, device=DEV))
+
+    def check_grads(self, accumulate):
+        check("x_grad", self.dx, self.want_dx, half_step(self.want_dx, self.dtype) * 1.01 + self.slack_dx)
+        want = self.want_dw + (self.old.double() if accumulate else 0.0)
+        check("table_grad", self.dw, want, half_step(want, self.dtype) * 1.01 + self.slack_dw + U * want.abs())
+        assert torch.equal(between(self.dx, self.dx_buf), self.rest[0])
+        assert torch.equal(between(self.dw, self.dw_buf), self.rest[1])
+
+    def outputs(self):
+        return [self.losses, self.loss, self.count, self.dx, self.dw]
+
+
+SIZES = [(1, 1, 1, 0, 0), (1, 300, 64, 0, 0), (3, 257, 40, 0, 0), (33, 1000, 129, 3, 1), (256, 512, 64, 8, 0),
+         (257, 255, 192, 0, 0), (300, 4099, 72, 1, 0), (700, 777, 1600, 0, 8), (64, 20_011, 264, 0, 0)]
+
+
+@pytest.mark.parametrize("dt", FORMATS)
+@pytest.mark.parametrize("tokens,vocab,cols,spare,shift", SIZES)
+def test_losses(tokens, vocab, cols, spare, shift, dt):
+    h = Head(tokens, vocab, cols, dt, spare, shift).want()
+    op = LossHead(h.table, max_tokens=tokens, gradients=False)
+    op.ws.fill_(0xFF)
+    op.forward(h.x, h.labels.int(), h.losses, h.loss, h.count)
+    h.check_losses()
+
+
+@pytest.mark.parametrize("dt", FORMATS)
+@pytest.mark.parametrize("tokens,vocab,cols,spare,shift", SIZES)
+def test_gradients(tokens, vocab, cols, spare, shift, dt):
+    state = torch.zeros(16, dtype=torch.float64, device=DEV)
+    Z.zero_step_state_init(state, 64.0, 1000)
+    for accumulate, sure in ((False, 0.0), (True, 12.0)):
+        h = Head(tokens, vocab, cols, dt, spare, shift, seed=int(sure), sure=sure)
+        with_state = dt == "fp16"
+        h.want(0.5 * (64.0 if with_state else 1.0))
+        op = LossHead(h.table, max_tokens=tokens + 300)
+        op.ws.fill_(0xFF)  # NaN wherever something is taken that nobody wrote
+        op.grad(h.x, h.labels, h.losses, h.loss, h.count, h.dx, h.dw, accumulate=accumulate,
+                step_state=state if with_state else None, scale=0.5)
+        h.check_losses()
+        h.check_grads(accumulate)
+        first = [t.clone() for t in h.outputs()]
+        h.dw.copy_(h.old)
+        op.grad(h.x, h.labels.int(), h.losses, h.loss, h.count, h.dx, h.dw, accumulate=accumulate,
+                step_state=state if with_state else None, scale=0.5)
+        assert all(torch.equal(a, b) for a, b in zip(first, h.outputs()))
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_more_tokens_than_one_block_holds(accumulate):
+    """A vocabulary of 2^18 + 1 words leaves blocks of 256 tokens: three of them, the last with one token."""
+    h = Head(513, (1 << 18) + 1, 24, "bf16", ignored=0.1).want(2.0)
+    op = LossHead(h.table, max_tokens=513)
+    op.ws.fill_(0xFF)
+    op.grad(h.x, h.labels, h.losses, h.loss, h.count, h.dx, h.dw, accumulate=accumulate, scale=2.0)
+    h.check_losses()
+    h.check_grads(accumulate)
+
+
+@pytest.mark.parametrize("dt", FORMATS)
+def test_no_token_counts(dt):
+    """All labels outside the vocabulary, and no tokens at all: losses and gradients of zeros, or nothing added."""
+    for tokens in (0, 5, 300):
+        h = Head(max(tokens, 1), 100, 64, dt)
+        x, losses, dx = h.x[:tokens], h.losses[:tokens], h.dx[:tokens]
+        x.fill_(float("nan"))  # their rows have no part in the gradients, whatever they hold
+        labels = torch.tensor([-1, 100, 2**40, -2**40, -100] * 60, device=DEV)[:tokens]
+        op = LossHead(h.table, max_tokens=tokens)
+        op.grad(x, labels, losses, h.loss, h.count, dx, h.dw, accumulate=True)
+        assert torch.equal(h.dw, h.old) and not dx.any() and not losses.any()
+        assert h.loss.item() == 0.0 and h.count.item() == 0
+        op.grad(x, labels, losses, h.loss, h.count, dx, h.dw)
+        assert not h.dw.any()
+
+
+def test_rows_that_do_not_count_may_hold_anything():
+    h = Head(290, 500, 136, "bf16", ignored=0.4)
+    h.x[h.labels < 0] = float("inf")
+    h.x[(h.labels < 0).nonzero()[:3, 0]] = float("nan")
+    h.want()
+    LossHead(h.table, max_tokens=290).grad(h.x, h.labels, h.losses, h.loss, h.count, h.dx, h.dw)
+    h.check_losses()
+    h.check_grads(False)
+
+
+def test_scores_that_are_not_finite():
+    """A word at -inf has probability 0; +inf and NaN make their token NaN and leave the others alone."""
+    h = Head(40, 300, 64, "bf16", ignored=0.0)
+    with torch.no_grad():
+        h.x[:, 0] = 0.0
+        h.x[3, 0] = float("nan")
+        h.x[5, 0] = 1.0
+        h.table[:, 0] = 0.0
+        h.table[7, 0] = float("-inf")  # 0 * inf is NaN: seen by every token
+    h.labels[:] = 9
+    op = LossHead(h.table, max_tokens=40)
+    op.forward(h.x, h.labels, h.losses, h.loss, h.count)
+    bad = h.losses.isnan()
+    assert bad[[0, 1, 3]].all()  # 0 * -inf
+    assert not bad[5]  # 1 * -inf = -inf
+    z = h.x[5].double() @ h.table.double().t()
+    assert abs(h.losses[5].item() - (torch.logsumexp(z, 0) - z[9]).item()) < 1e-4
+    h.table[7, 0] = 0.0
+    h.x[3, 0] = 1.0
+    h.x[8] = float("nan")
+    op.grad(h.x, h.labels, h.losses, h.loss, h.count, h.dx, h.dw)
+    bad = h.losses.isnan()
+    assert bad.nonzero()[:, 0].tolist() == [8] and h.loss.isnan()
+    assert h.dx[8].isnan().all() and h.dx[torch.arange(40, device=DEV) != 8].isfinite().all()
+    assert h.dw.isnan().all()
+
+
+def test_scores_far_apart():
+    """Scores over hundreds of octaves: no overflow, no loss of the words near the maximum."""
+    h = Head(70, 700, 64, "bf16", sigma=4.0, ignored=0.0).want()
+    LossHead(h.table, max_tokens=70).grad(h.x, h.labels, h.losses, h.loss, h.count, h.dx, h.dw)
+    h.check_losses()
+    h.check_grads(False)
+
+
+def test_gradients_against_differences():
+    """Central differences of the loss in 64 bits; the factors are off by 2^-9 of themselves, so the sums by 2^-8 of
+    the largest gradient at most."""
+    h = Head(6, 40, 16, "fp16", ignored=0.0, sigma=0.3).want()
+    LossHead(h.table, max_tokens=6).grad(h.x, h.labels, h.losses, h.loss, h.count, h.dx, h.dw)
+
+    def loss(x, w):
+        z = x @ w.t()
+        return (torch.logsumexp(z, 1) - z.gather(1, h.labels[:, None])[:, 0]).mean().item()
+
+    point, step = [h.x.double(), h.table.double()], 1e-5
+    for k, grad in enumerate((h.dx, h.dw)):
+        for i in range(0, point[k].numel(), 11):
+            found = []
+            for sign in (1, -1):
+                moved = [p.clone() for p in point]
+                moved[k].view(-1)[i] += sign * step
+                found.append(loss(*moved))
+            want = (found[0] - found[1]) / (2 * step)
+            assert abs(grad.reshape(-1)[i].item() - want) <= 2.0**-8 * grad.abs().max().item(), (k, i)
