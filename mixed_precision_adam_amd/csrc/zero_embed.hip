@@ -514,7 +514,7 @@ int zero_embed_grad(const void* ids_dev, int32_t id_bytes, int64_t first_row, co
   const int64_t fills = accumulate ? 0 : ceil_div(rows, kFillRows);
   const int64_t tiles = ceil_div(cols, kTileCols);
   const int64_t sums = tokens <= kFew ? tokens * tiles : ceil_div(static_cast<int64_t>(w.c.chunks) * tiles, 4);
-  if (tiles > (int64_t(1) << 15) || sums + fills > (int64_t(1) << 30))
+  if (tiles * std::max<int64_t>(w.c.chunks, 1) >= kLaunchGroups || sums + fills >= kLaunchGroups)
     return fail(ZERO_ERR_INVALID, "%s: too many rows or columns for one launch", fn);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(sums + fills)), block(kBlock);

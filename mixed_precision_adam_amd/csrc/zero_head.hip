@@ -573,7 +573,8 @@ bool direct(const zero_rows* r) {
 }
 
 bool head_sizes_ok(int64_t tokens, int64_t vocab, int64_t cols) {
-  return sizes_ok(tokens, cols) && vocab >= 1 && vocab <= kMostVocab && cols <= kMostCols;
+  return sizes_ok(tokens, cols) && vocab >= 1 && vocab <= kMostVocab && cols <= kMostCols &&
+         round_up(vocab, kTileN) / 64 * ceil_div(cols, 64) < kLaunchGroups;
 }
 
 struct Call {

@@ -172,6 +172,10 @@ int with_dtype(int dt, F&& f) {
   }
 }
 
+// Workgroups of kBlock threads that a launch can have: its threads are counted
+// in 32 bits.
+constexpr int64_t kLaunchGroups = (int64_t(1) << 32) / kBlock;
+
 inline bool any_dtype_ok(int dt) { return dtype_ok(dt) || dt == ZERO_FP32; }
 inline int64_t dtype_bytes(int dt) { return dt == ZERO_FP32 ? 4 : 2; }
 inline bool unaligned(const void* p, uintptr_t align) { return (reinterpret_cast<uintptr_t>(p) & (align - 1)) != 0; }
