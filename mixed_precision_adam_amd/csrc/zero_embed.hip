@@ -232,7 +232,7 @@ __global__ __launch_bounds__(kBlock) void sort_pass_kernel(const void* __restric
     const uint32_t row = local_row(ids, id_bytes, t, first, rows);
     return make_uint2(row == kNoRow ? static_cast<uint32_t>(rows) : row, t);
   };
-  for (uint32_t k = threadIdx.x; k < 4 * kMaxDigits; k += kBlock) at[0][k] = 0;
+  for (uint32_t k = threadIdx.x; k < 4 * kMaxDigits; k += kBlock) at[k / kMaxDigits][k % kMaxDigits] = 0;
   __syncthreads();
   for (uint32_t t = lo + lane; t < hi; t += 64) atomicAdd(&at[wave][(item(t).x >> shift) & (digits - 1)], 1u);
   __syncthreads();

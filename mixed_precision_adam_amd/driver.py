@@ -607,7 +607,8 @@ class LossHead(_Operator):
             raise ValueError(f"{x.shape[0]} tokens, made for {self.max_tokens} (max_tokens)")
 
     def forward(self, x, labels, losses, loss, count, stream=None) -> None:
-        """losses[t] (fp32; 0 where the label does not count), their mean in `loss` (fp32) and how many count (int64)."""
+        """losses[t] (fp32; 0 where the label does not count), their mean in `loss` (fp32), and how many count (int64)
+        in `count`."""
         self._on(x, labels, losses, loss, count)
         self._fits(x)
         self._call(zero_loss_head, x, self.table, labels, losses, loss, count, self.ws, self.ws_bytes, stream=stream)

@@ -1,0 +1,72 @@
+"""Code generation of the embedding, layer norm and loss head kernels (CPU only: compiles the sources to gfx950 assembly
+with the library's own flags).
+
+* Memory accesses are global, not flat (but for the places in LDS that a pass of the sort reads and writes as volatile).
+* Units move in 16-byte accesses; the products load straight into LDS and multiply on the matrix cores, and wait for
+  loads only where a step meets; they keep everything in registers.
+* The rules on scalar memory and packed arithmetic that hold for the library's other sources."""
+import os
+import re
+import subprocess
+
+import pytest
+
+from mixed_precision_adam_amd import build as B
+from tests import test_codegen
+
+SOURCES = {"embed": B.EMBED_SRC, "norm": B.NORM_SRC, "head": B.HEAD_SRC}
+
+
+@pytest.fixture(scope="module")
+def asm(tmp_path_factory):
+    if not os.path.exists(B.HIPCC):
+        pytest.skip("hipcc not available")
+    folder = tmp_path_factory.mktemp("asm")
+    flags = [f for f in B.FLAGS if f != "-fPIC"]
+    runs = {}
+    for name, src in SOURCES.items():
+        out = str(folder / f"{name}.s")
+        runs[out] = name, subprocess.Popen([B.HIPCC, *flags, "-I", os.path.join(B.ROOT, "include"),
+                                            "--cuda-device-only", "-S", "-o", out, src], stderr=subprocess.DEVNULL)
+    for _, p in runs.values():
+        assert p.wait() == 0
+    return {name: open(out).read() for out, (name, _) in runs.items()}
+
+
+@pytest.mark.parametrize("source", SOURCES)
+def test_no_flat_accesses(asm, source):
+    for name, body in test_codegen.kernels(asm[source]).items():
+        assert "sort_pass_kernel" in name or not [x for x in body if x.startswith("flat_")], name
+
+
+@pytest.mark.parametrize("source,kernel", [("embed", "embed_forward_kernel"), ("embed", "embed_grad_few_kernel"),
+                                           ("embed", "embed_grad_kernel"), ("norm", "layernorm_forward_kernel"),
+                                           ("norm", "layernorm_grad_kernel")])
+def test_units_move_in_16_bytes(asm, source, kernel):
+    found = [(n, b) for n, b in test_codegen.kernels(asm[source]).items() if kernel in n]
+    assert found
+    for name, body in found:
+        for access in ("load", "store"):
+            assert [x for x in body if re.match(rf"global_{access}_dwordx4\b", x)], (name, access)
+
+
+def test_products_run_on_the_matrix_cores(asm):
+    found = {n: b for n, b in test_codegen.kernels(asm["head"]).items()
+             if re.search(r"(scores|x_grad|table_grad)_kernel", n)}
+    assert len(found) == 6  # three products, two formats
+    for name, body in found.items():
+        assert not [x for x in body if x.startswith("scratch_")], name
+        kind = "bf16" if "ILi0E" in name else "f16"
+        assert sum(x.startswith(f"v_mfma_f32_16x16x32_{kind}") for x in body) >= 128, name
+        assert [x for x in body if re.match(r"buffer_load_dwordx4 .* lds$", x)], name
+        # in the loop: a wait for loads directly before a barrier, and nowhere else
+        first, last = (f(k for k, x in enumerate(body) if x.startswith("v_mfma")) for f in (min, max))
+        loop = body[first:last]
+        for k, x in enumerate(loop):
+            if x.startswith("s_waitcnt") and "vmcnt" in x:
+                assert any(y.startswith("s_barrier") for y in loop[k:k + 4]), (name, loop[k:k + 4])
+
+
+@pytest.mark.parametrize("source", SOURCES)
+def test_no_scalar_memory_writes_and_no_packed_fp32(asm, source):
+    test_codegen.test_no_scalar_memory_writes_and_no_packed_fp32(asm[source])

@@ -35,8 +35,9 @@ def test_structure_matches_the_header(tmp_path):
 
 
 # What no zero_rows may be, and a word of the message.
-BAD_ROWS = [(dict(dt=3), "dtype"), (dict(dt=-1), "dtype"), (dict(n=-1), "out of range"), (dict(n=2**31), "out of range"),
-            (dict(cols=0), "out of range"), (dict(cols=2**31), "out of range"), (dict(stride=7), "out of range"),
+BAD_ROWS = [(dict(dt=3), "dtype"), (dict(dt=-1), "dtype"), (dict(n=-1), "out of range"),
+            (dict(n=2**31), "out of range"), (dict(cols=0), "out of range"), (dict(cols=2**31), "out of range"),
+            (dict(stride=7), "out of range"),
             (dict(stride=2**40), "out of range"), (dict(stride=-8), "out of range"), (dict(data=None), "no data"),
             (dict(data=4097), "aligned"), (dict(data=4098, dt=Z.ZERO_FP32), "aligned")]
 
