@@ -504,6 +504,22 @@ struct Space {
   size_t factor, label_score, lse, pieces, x, table, codes, turned, x_turned, table_turned, parts, sums, bytes;
 };
 
+// How many parts the sum over the vocabulary is split into: the number that
+// takes the fewest rounds of steps over the CUs.  A workgroup costs about 12
+// steps besides its own (filling its buffers, writing its part).
+int split_count(int64_t tiles, int64_t steps) {
+  int best = 1;
+  int64_t least = std::numeric_limits<int64_t>::max();
+  for (int64_t s = 1; s <= std::min(std::max<int64_t>(kMostParts / tiles, 1), steps); ++s) {
+    const int64_t cost = ceil_div(tiles * s, kCus) * (ceil_div(steps, s) + 12);
+    if (cost < least) {
+      least = cost;
+      best = static_cast<int>(s);
+    }
+  }
+  return best;
+}
+
 Space space_of(int64_t tokens, int64_t vocab, int64_t cols, bool gradients) {
   Space s{};
   s.k = round_up(cols, kStep);
@@ -529,29 +545,17 @@ Space space_of(int64_t tokens, int64_t vocab, int64_t cols, bool gradients) {
     s.turned = part(2 * s.block * s.vocab_padded);
     s.x_turned = part(2 * s.block * cols);
     s.table_turned = part(2 * s.vocab_padded * cols);
-    // kMostParts tiles in all, or one for each tile of the result
-    const int64_t tiles = ceil_div(s.block, kTileM) * ceil_div(cols, kTileN);
-    s.parts = part(4 * std::max<int64_t>(kMostParts, tiles) * kTileM * round_up(kTileN, 8));
+    // The most that a block of as many tokens or fewer splits into.
+    int64_t rows = 0;
+    for (int64_t m = kTileM; m <= s.block; m += kTileM) {
+      const int splits = split_count(m / kTileM * ceil_div(cols, kTileN), s.vocab_padded / kStep);
+      rows = std::max(rows, splits * std::min(m, std::max<int64_t>(tokens, 1)));
+    }
+    s.parts = part(4 * rows * s.part_stride);
     s.sums = part(tokens > s.block ? 4 * vocab * s.part_stride : 0);
   }
   s.bytes = at;
   return s;
-}
-
-// How many parts the sum over the vocabulary is split into: the number that
-// takes the fewest rounds of steps over the CUs.  A workgroup costs about 12
-// steps besides its own (filling its buffers, writing its part).
-int split_count(int64_t tiles, int64_t steps) {
-  int best = 1;
-  int64_t least = std::numeric_limits<int64_t>::max();
-  for (int64_t s = 1; s <= std::min(std::max<int64_t>(kMostParts / tiles, 1), steps); ++s) {
-    const int64_t cost = ceil_div(tiles * s, kCus) * (ceil_div(steps, s) + 12);
-    if (cost < least) {
-      least = cost;
-      best = static_cast<int>(s);
-    }
-  }
-  return best;
 }
 
 Product product(Operand a, Operand b, int64_t k, int splits) {

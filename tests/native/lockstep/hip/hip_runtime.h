@@ -270,7 +270,7 @@ void load_lds(const Buffer& r, Lds lds, uint32_t voffset, uint32_t soffset) {
 #define blockIdx (lockstep::block)
 #define gridDim (lockstep::blocks)
 #define hipLaunchKernelGGL(kernel, grid, group, lds, stream, ...) \
-  lockstep::launch(grid, group, [&, st = (stream)] { (void)st; kernel(__VA_ARGS__); })
+  lockstep::launch(grid, group, [&, lockstep_stream = (stream)] { (void)lockstep_stream; kernel(__VA_ARGS__); })
 #define __syncthreads() (void)lockstep::barrier(0)
 #define __syncthreads_or(p) lockstep::barrier((p) ? 1 : 0)
 #define __ballot(p) lockstep::ballot((p), __LINE__)
