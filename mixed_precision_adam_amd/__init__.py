@@ -568,41 +568,44 @@ _ID_BYTES = {torch.int32: 4, torch.int64: 8}
 
 def _rows(x, name: str = "rows") -> zero_rows:
     """The zero_rows of a 2-D tensor whose rows are contiguous (a zero_rows is taken as it is)."""
-    if isinstance(x, zero_rows):
+    if type(x) is zero_rows:
         return x
-    if not x.is_cuda:
-        raise ValueError(f"{name}: a GPU tensor is required, got one on {x.device}")
-    if x.dim() != 2 or x.dtype not in _FORMAT:
-        raise ValueError(f"{name}: a matrix in bf16, fp16 or fp32 is required, got {x.dtype} {tuple(x.shape)}")
-    rows, cols = x.shape
+    shape, dt = x.shape, _FORMAT.get(x.dtype)
+    if dt is None or len(shape) != 2 or not x.is_cuda:
+        if not x.is_cuda:
+            raise ValueError(f"{name}: a GPU tensor is required, got one on {x.device}")
+        raise ValueError(f"{name}: a matrix in bf16, fp16 or fp32 is required, got {x.dtype} {tuple(shape)}")
+    rows, cols = shape
     stride, step = x.stride()
     if step != 1 and cols > 1:
-        raise ValueError(f"{name}: rows must be contiguous, got strides {tuple(x.stride())}")
+        raise ValueError(f"{name}: rows must be contiguous, got strides {(stride, step)}")
     if rows <= 1:
         stride = cols
     elif stride < cols:
-        raise ValueError(f"{name}: rows overlap, strides {tuple(x.stride())}")
-    return zero_rows(x.data_ptr(), rows, cols, stride, _FORMAT[x.dtype], 0)
+        raise ValueError(f"{name}: rows overlap, strides {(stride, step)}")
+    return zero_rows(x.data_ptr(), rows, cols, stride, dt, 0)
 
 
 def _ids(x, n: int):
     """(address, bytes of one) of n contiguous int32 or int64."""
-    if x.dtype not in _ID_BYTES:
+    size = _ID_BYTES.get(x.dtype)
+    if size is None:
         raise ValueError(f"int32 or int64 is required, got {x.dtype}")
     if x.numel() != n:
         raise ValueError(f"{x.numel()} tokens for {n} rows")
-    return _addr(x), _ID_BYTES[x.dtype]
+    return _addr(x), size
 
 
 def _vector(x, n: int, name: str, formats=_FORMAT):
     """(address, format) of n contiguous elements, or (None, None)."""
     if x is None:
         return None, None
-    if x.dtype not in formats:
+    dt = formats.get(x.dtype)
+    if dt is None:
         raise ValueError(f"{name}: dtype {x.dtype} where one of {sorted(map(str, formats))} is needed")
     if x.numel() != n:
         raise ValueError(f"{name}: {x.numel()} elements where {n} are needed")
-    return _addr(x), _FORMAT[x.dtype]
+    return _addr(x), dt
 
 
 _FP32_ONLY = {torch.float32: ZERO_FP32}

@@ -41,6 +41,7 @@ _TORCH16 = {ZERO_BF16: torch.bfloat16, ZERO_FP16: torch.float16}
 # The current stream's handle without building a torch.cuda.Stream: 0.1 instead of 2.7 us, in calls of 5.
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 @dataclass
@@ -516,7 +517,7 @@ class _Operator:
             stream = _current_raw_stream(self.device.index)
         elif not isinstance(stream, int) and getattr(stream, "device", self.device) != self.device:
             raise ValueError(f"a stream of {stream.device} for an operator on {self.device}")
-        if torch.cuda.current_device() == self.device.index:
+        if _current_device() == self.device.index:
             fn(*args, stream=stream, **more)
         else:  # kernels are launched from the device that holds the tensors
             with torch.cuda.device(self.device):
