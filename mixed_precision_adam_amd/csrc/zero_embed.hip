@@ -26,7 +26,10 @@ using namespace zero_detail;
 
 constexpr int64_t kMaxGroups = int64_t(1) << 20;  // workgroups of one launch; they stride over what is left
 
-// One workgroup copies `per` tokens' rows at a time, unit by unit.
+// One workgroup copies `per` tokens' rows at a time, unit by unit: four units a
+// thread in flight at once.  Bound by HBM: 16384 rows of 4096 bf16 in 54 us a
+// call (5.0 TB/s; a copy between two buffers makes 4.7), 8 rows of 1600 in 7.3,
+// which is the call's host time.
 template <int TD, int OD>
 __global__ __launch_bounds__(kBlock) void embed_forward_kernel(Rows table, int64_t first, const void* __restrict__ ids,
                                                                int id_bytes, float scale, Rows out, uint32_t per,
@@ -54,6 +57,9 @@ __global__ __launch_bounds__(kBlock) void embed_forward_kernel(Rows table, int64
 // and rows of dW written once; everything else is small.  A row of dW belongs
 // to one wavefront (one column tile of 512 at a time), which adds its tokens'
 // rows in the order of the text: no atomics on sums, so no order of arrival.
+// Measured, calls behind one another: 301 tokens added to 50257x1600 bf16 8.3 us
+// (one launch), 8192 tokens and every row written 81 us (2.3 TB/s of rows),
+// 32769 tokens of 5120 fp16 added to an fp32 half table 148 us (3.4 TB/s).
 
 constexpr int kTileCols = 512;  // 64 lanes of one unit
 constexpr int kFillRows = 64;   // rows of dW that one workgroup looks over for rows without tokens
@@ -84,7 +90,9 @@ __device__ __forceinline__ void fill_rows(const Rows& dw, int64_t row0, uint64_t
   }
 }
 
-// Up to kFew tokens: no sort.  A workgroup belongs to one token and column
+// Up to kFew tokens: no sort, one launch where the sorted form has five or six
+// (the border lies where every workgroup's look over all tokens is still a few
+// loads a thread; other borders were not measured).  A workgroup belongs to one token and column
 // tile; unless an earlier token has the same row it finds the others by
 // comparing, its four wavefronts add a quarter of them each, and the quarters
 // are joined in order.  Workgroups from `sums` on fill the rows without tokens.
