@@ -691,7 +691,9 @@ int zero_loss_head(const zero_rows* x, const zero_rows* table, const void* label
  *                            holds with accumulate
  * loss_scale is state_dev->loss_scale when the kernels run (1 where state_dev
  * is NULL), so a captured step follows the scale that the decision moves.  The
- * factors softmax - onehot are rounded to the 16-bit format for the products.
+ * factors softmax - onehot are rounded to the 16-bit format for the products,
+ * from scores held to 2^-12 of an octave (a word more than 32 octaves below the
+ * largest of its 64 neighbours counts as 0 there).
  * A token that does not count has no part in the gradients, whatever its row
  * of x holds. */
 int zero_loss_head_grad(const zero_rows* x, const zero_rows* table, const void* labels_dev, int32_t label_bytes,
