@@ -554,6 +554,8 @@ class TokenEmbedding(_Operator):
 
     def grad(self, ids, out_grad, table_grad, accumulate: bool = False, stream=None) -> None:
         """The table's gradient (any format and row stride), in place of what `table_grad` holds or added to it."""
+        if not self.max_tokens:
+            raise ValueError("made without gradients (max_tokens=0)")
         self._on(ids, out_grad, table_grad)
         if table_grad.shape != self.table.shape:
             raise ValueError(f"a gradient of {tuple(table_grad.shape)} for a table of {tuple(self.table.shape)}")

@@ -241,3 +241,13 @@ def test_operators_check_what_they_are_made_of():
         driver.LayerNorm(torch.zeros(16385))
     with pytest.raises(ValueError, match="out of range"):
         driver.TokenEmbedding(torch.zeros(4, 0), max_tokens=4)
+
+
+@pytest.mark.parametrize("tokens", [0, 3])
+def test_an_embedding_without_max_tokens_refuses_gradients(tokens):
+    """It has no workspace, so not even the gradient of no tokens at all is taken."""
+    table = torch.zeros(4, 8)
+    op = driver.TokenEmbedding(table)
+    op._on = lambda *tensors: None  # the tensors stand for ones on the operator's GPU
+    with pytest.raises(ValueError, match="max_tokens"):
+        op.grad(torch.zeros(tokens, dtype=torch.int64), torch.zeros(tokens, 8), table)
