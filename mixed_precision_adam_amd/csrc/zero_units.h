@@ -112,26 +112,32 @@ struct Unit {
       }
     }
   }
+  // The words are copied before one is chosen: a choice between elements of w would be one between addresses, and would
+  // put the unit into scratch memory, whole units' stores included.
   __device__ __forceinline__ void store_part(void* p, int n) const {
+    const uint32_t w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3];
     if constexpr (DT == ZERO_FP32) {
+      const uint32_t w4 = w[4], w5 = w[5], w6 = w[6];
       uint32_t* q = static_cast<uint32_t*>(p);
       if (n & 4) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) q[k] = w[k];
+        q[0] = w0;
+        q[1] = w1;
+        q[2] = w2;
+        q[3] = w3;
       }
       if (n & 2) {
-        q[n & 4] = n & 4 ? w[4] : w[0];
-        q[(n & 4) + 1] = n & 4 ? w[5] : w[1];
+        q[n & 4] = n & 4 ? w4 : w0;
+        q[(n & 4) + 1] = n & 4 ? w5 : w1;
       }
-      if (n & 1) q[n - 1] = n == 1 ? w[0] : n == 3 ? w[2] : n == 5 ? w[4] : w[6];
+      if (n & 1) q[n - 1] = n == 1 ? w0 : n == 3 ? w2 : n == 5 ? w4 : w6;
     } else {
       uint16_t* q = static_cast<uint16_t*>(p);
       if (n & 4) {
-        *reinterpret_cast<u32_any*>(q) = w[0];
-        *reinterpret_cast<u32_any*>(q + 2) = w[1];
+        *reinterpret_cast<u32_any*>(q) = w0;
+        *reinterpret_cast<u32_any*>(q + 2) = w1;
       }
-      if (n & 2) *reinterpret_cast<u32_any*>(q + (n & 4)) = n & 4 ? w[2] : w[0];
-      if (n & 1) q[n - 1] = static_cast<uint16_t>(n == 1 ? w[0] : n == 3 ? w[1] : n == 5 ? w[2] : w[3]);
+      if (n & 2) *reinterpret_cast<u32_any*>(q + (n & 4)) = n & 4 ? w2 : w0;
+      if (n & 1) q[n - 1] = static_cast<uint16_t>(n == 1 ? w0 : n == 3 ? w1 : n == 5 ? w2 : w3);
     }
   }
   // Rounds once, to nearest.  Elements are set in order: the even one of a

@@ -70,3 +70,17 @@ def test_products_run_on_the_matrix_cores(asm):
 @pytest.mark.parametrize("source", SOURCES)
 def test_no_scalar_memory_writes_and_no_packed_fp32(asm, source):
     test_codegen.test_no_scalar_memory_writes_and_no_packed_fp32(asm[source])
+
+
+RAGGED_8_UNITS = re.compile(r"layernorm_grad_kernelILi\dELi8ELi4ELb1E")
+
+
+def scratch(body):
+    return [x for x in body if x.startswith("scratch_")]
+
+
+@pytest.mark.parametrize("source", SOURCES)
+def test_stores_do_not_go_through_scratch_memory(asm, source):
+    """Units stay in registers up to their store, whole rows and ragged ones."""
+    for name, body in test_codegen.kernels(asm[source]).items():
+        assert RAGGED_8_UNITS.search(name) or not scratch(body), (name, scratch(body)[:3])
