@@ -60,10 +60,19 @@ __device__ __forceinline__ int lane_unit(int k) {
   return WPR > 1 ? k * kBlock + static_cast<int>(threadIdx.x) : k * 64 + static_cast<int>(threadIdx.x & 63);
 }
 
-// Elements of a unit: without TAIL the rows are whole units, and the code for
-// part of one (a third of the kernels' registers) is left out.
-template <bool TAIL>
-__device__ __forceinline__ int norm_unit_size(int64_t cols, int u) {
+// Units of a lane that every row of the form's range has in full: with_row_shape
+// gives a row to the first form whose NU units a lane hold it, so a row is longer
+// than what the next smaller form holds (NU - 1 units a lane, or 4 below 8).
+template <int NU>
+constexpr int kWholeUnits = NU == 8 ? 4 : NU - 1;
+
+// Elements of a lane's unit k, which is the row's unit u.  Without TAIL the rows
+// are whole units, and the code for part of one (a third of the kernels'
+// registers) is left out; with it only a lane's last units carry that code (in
+// all of them it sent rows of 8193 to 16384 ragged columns to scratch memory).
+template <int NU, bool TAIL>
+__device__ __forceinline__ int norm_unit_size(int64_t cols, int k, int u) {
+  if (k < kWholeUnits<NU>) return 8;
   return TAIL ? unit_size(cols, u) : static_cast<int64_t>(u) * 8 < cols ? 8 : 0;
 }
 
@@ -100,7 +109,7 @@ __global__ __launch_bounds__(kBlock) void layernorm_forward_kernel(Rows x, const
     float sum = 0.0f, none = 0.0f;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      const int u = lane_unit<WPR>(k), n = norm_unit_size<TAIL>(x.cols, u);
+      const int u = lane_unit<WPR>(k), n = norm_unit_size<NU, TAIL>(x.cols, k, u);
       v[k].clear();
       if (n > 0) v[k].load(x.at<DT>(row, static_cast<int64_t>(u) * 8), n);
     }
@@ -116,7 +125,7 @@ __global__ __launch_bounds__(kBlock) void layernorm_forward_kernel(Rows x, const
     float sq = 0.0f;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      const int n = norm_unit_size<TAIL>(x.cols, lane_unit<WPR>(k));
+      const int n = norm_unit_size<NU, TAIL>(x.cols, k, lane_unit<WPR>(k));
       if (n >= 8) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) sq += (v[k].get(i) - mu) * (v[k].get(i) - mu);
@@ -129,7 +138,7 @@ __global__ __launch_bounds__(kBlock) void layernorm_forward_kernel(Rows x, const
     const float r = 1.0f / sqrtf(sq * inv + eps);
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      const int u = lane_unit<WPR>(k), n = norm_unit_size<TAIL>(x.cols, u);
+      const int u = lane_unit<WPR>(k), n = norm_unit_size<NU, TAIL>(x.cols, k, u);
       if (n > 0) {
         const int64_t col = static_cast<int64_t>(u) * 8;
         float w[8], b[8];
@@ -171,7 +180,7 @@ __global__ __launch_bounds__(kBlock) void layernorm_grad_kernel(Rows x, Rows dy,
     Unit<DT> a[NU], g[NU];
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      const int u = lane_unit<WPR>(k), n = norm_unit_size<TAIL>(x.cols, u);
+      const int u = lane_unit<WPR>(k), n = norm_unit_size<NU, TAIL>(x.cols, k, u);
       a[k].clear();
       g[k].clear();
       if (n > 0) {
@@ -183,7 +192,7 @@ __global__ __launch_bounds__(kBlock) void layernorm_grad_kernel(Rows x, Rows dy,
     float level = 0.0f, along = 0.0f;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      const int u = lane_unit<WPR>(k), n = norm_unit_size<TAIL>(x.cols, u);
+      const int u = lane_unit<WPR>(k), n = norm_unit_size<NU, TAIL>(x.cols, k, u);
       float w[8] = {};
       if (n > 0 && dx.data) load_weight<DT>(weight, w32 != 0, static_cast<int64_t>(u) * 8, n, w);
 #pragma unroll
@@ -201,7 +210,7 @@ __global__ __launch_bounds__(kBlock) void layernorm_grad_kernel(Rows x, Rows dy,
     along *= inv;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      const int u = lane_unit<WPR>(k), n = norm_unit_size<TAIL>(x.cols, u);
+      const int u = lane_unit<WPR>(k), n = norm_unit_size<NU, TAIL>(x.cols, k, u);
       if (n > 0) {
         float w[8];
         load_weight<DT>(weight, w32 != 0, static_cast<int64_t>(u) * 8, n, w);

@@ -84,3 +84,11 @@ def test_stores_do_not_go_through_scratch_memory(asm, source):
     """Units stay in registers up to their store, whole rows and ragged ones."""
     for name, body in test_codegen.kernels(asm[source]).items():
         assert RAGGED_8_UNITS.search(name) or not scratch(body), (name, scratch(body)[:3])
+
+
+def test_ragged_rows_of_eight_units_a_lane_stay_in_registers(asm):
+    """Layer norm's backward pass over 8193 to 16384 ragged columns: the widest form, in each format."""
+    found = {n: b for n, b in test_codegen.kernels(asm["norm"]).items() if RAGGED_8_UNITS.search(n)}
+    assert len(found) == 3
+    for name, body in found.items():
+        assert not scratch(body), (name, len(scratch(body)))
