@@ -280,7 +280,13 @@ __global__ __launch_bounds__(kBlock) void sort_pass_kernel(const void* __restric
   }
   __syncthreads();
   uint32_t* next = counts + static_cast<size_t>(pass + 1) * kSortBlocks * kMaxDigits;
-  volatile uint32_t* place = at[wave];  // only this wavefront's from here on
+  // Only this wavefront reads and writes its digits' places from here on, in LDS, which keeps a wavefront's accesses in
+  // order: what is needed is that the compiler keeps it too, once the places are read and once they are moved on.
+  const auto in_order = [] {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
   for (uint32_t t0 = lo; t0 < hi; t0 += 64) {
     const bool some = t0 + lane < hi;
     const uint2 kv = some ? item(t0 + lane) : make_uint2(0, 0);
@@ -291,17 +297,17 @@ __global__ __launch_bounds__(kBlock) void sort_pass_kernel(const void* __restric
       same &= (digit >> b) & 1u ? ones : ~ones;
     }
     const uint32_t rank = __popcll(same & ((1ull << lane) - 1)), many = __popcll(same);
-    const uint32_t start = some ? place[digit] : 0u;
-    __builtin_amdgcn_wave_barrier();
+    const uint32_t start = some ? at[wave][digit] : 0u;
+    in_order();
     if (some) {
-      if (rank == 0) place[digit] = start + many;
+      if (rank == 0) at[wave][digit] = start + many;
       const uint32_t p = start + rank;
       to[p] = kv;
       if (pass == 0 && kv.x < rows && !((met[kv.x >> 5] >> (kv.x & 31)) & 1u)) atomicOr(&met[kv.x >> 5], 1u << (kv.x & 31));
       if (pass + 1 < s.passes)
         atomicAdd(&next[static_cast<size_t>(p / s.per_block) * kMaxDigits + ((kv.x >> (shift + s.digit_bits)) & (digits - 1))], 1u);
     }
-    __builtin_amdgcn_wave_barrier();
+    in_order();
   }
 }
 

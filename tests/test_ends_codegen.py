@@ -1,7 +1,7 @@
 """Code generation of the embedding, layer norm and loss head kernels (CPU only: compiles the sources to gfx950 assembly
 with the library's own flags).
 
-* Memory accesses are global, not flat (but for the places in LDS that a pass of the sort reads and writes as volatile).
+* Memory accesses are global, not flat, and nothing spills to scratch memory.
 * Units move in 16-byte accesses; the products load straight into LDS and multiply on the matrix cores, and wait for
   loads only where a step meets; they keep everything in registers.
 * The rules on scalar memory and packed arithmetic that hold for the library's other sources."""
@@ -92,3 +92,10 @@ def test_ragged_rows_of_eight_units_a_lane_stay_in_registers(asm):
     assert len(found) == 3
     for name, body in found.items():
         assert not scratch(body), (name, len(scratch(body)))
+
+
+def test_the_sort_reads_and_writes_its_places_as_lds(asm):
+    """No flat access in a pass of the sort either: each would wait for the wavefront's global stores and atomics."""
+    found = [b for n, b in test_codegen.kernels(asm["embed"]).items() if "sort_pass_kernel" in n]
+    assert len(found) == 1 and not [x for x in found[0] if x.startswith("flat_")]
+    assert [x for x in found[0] if x.startswith("ds_write_b32")]
