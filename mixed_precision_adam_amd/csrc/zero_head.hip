@@ -88,6 +88,14 @@ __device__ __forceinline__ void stage(__amdgpu_buffer_rsrc_t rows, char* lds, co
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rows, (lds_ptr)(lds + j * 8192 + wave * 1024), 16, at[j], step * 128, 0, 0);
 }
 
+// A wavefront's loads into LDS have landed before it meets the others: staged
+// data is there for all of them behind this.  The barrier alone promises that
+// only as far as the compiler counts these loads among what it has to wait for.
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0); the other counters are left as they are
+  __syncthreads();
+}
+
 template <int DT>
 struct Tile {
   f32x4 acc[kBlocksM][kBlocksN];
@@ -137,13 +145,13 @@ struct Tile {
     stage(rb, b0, vb, lo);
 #pragma unroll 1
     for (int s = lo; s < hi; s += 2) {
-      __syncthreads();  // step s has arrived, and nobody reads the other buffers any more
+      meet();  // step s has arrived, and nobody reads the other buffers any more
       if (s + 1 < hi) {
         stage(ra, a1, va, s + 1);
         stage(rb, b1, vb, s + 1);
       }
       add_step(a0, b0);
-      __syncthreads();
+      meet();
       if (s + 1 < hi) {
         if (s + 2 < hi) {
           stage(ra, a0, va, s + 2);

@@ -281,6 +281,7 @@ void load_lds(const Buffer& r, Lds lds, uint32_t voffset, uint32_t soffset) {
 #define __builtin_amdgcn_readfirstlane(v) lockstep::lanes(lockstep::kFirst, __LINE__, static_cast<int>(v), 0)
 #define __builtin_amdgcn_wave_barrier() (void)lockstep::ask(lockstep::kMeet, __LINE__, lockstep::Vec{})
 #define __builtin_amdgcn_fence(order, scope) (void)0
+#define __builtin_amdgcn_s_waitcnt(counters) (void)0
 #define __builtin_amdgcn_exp2f(x) exp2f(x)
 #define __builtin_amdgcn_logf(x) log2f(x)
 #define __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, x, y, z) lockstep::matrix(lockstep::kMfmaBf16, __LINE__, a, b, c)

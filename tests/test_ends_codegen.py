@@ -99,3 +99,49 @@ def test_the_sort_reads_and_writes_its_places_as_lds(asm):
     found = [b for n, b in test_codegen.kernels(asm["embed"]).items() if "sort_pass_kernel" in n]
     assert len(found) == 1 and not [x for x in found[0] if x.startswith("flat_")]
     assert [x for x in found[0] if x.startswith("ds_write_b32")]
+
+
+def unwaited_barriers(text):
+    """Barriers of a kernel that loads into LDS may pass before they have landed, over all its barriers from the first
+    such load on.  Going back from a barrier there has to be a wait for all loads before any load into LDS, and before
+    any label or branch, past which another way may lead to the barrier."""
+    lines = [x.split(";")[0].strip() for x in text.splitlines()]
+    lines = [x for x in lines if x]
+    loads = [k for k, x in enumerate(lines) if re.match(r"buffer_load_\w+ .* lds$", x)]
+    barriers = [k for k, x in enumerate(lines) if x.startswith("s_barrier") and loads and k > loads[0]]
+    bad = []
+    for k in barriers:
+        for x in reversed(lines[:k]):
+            if re.match(r"s_waitcnt .*\bvmcnt\(0\)", x):
+                break
+            if x.endswith(":") or re.match(r"(s_c?branch|s_barrier|buffer_load_\w+ .* lds$)", x):
+                bad.append(k)
+                break
+    return barriers, bad
+
+
+def test_staged_data_has_landed_at_every_barrier_of_the_products(asm):
+    text = asm["head"]
+    found = 0
+    for m in re.finditer(r"^(_Z\S*(?:scores|x_grad|table_grad)_kernel\S*):\s*;\s*@", text, re.M):
+        body = text[m.end():text.index(".Lfunc_end", m.end())]
+        barriers, bad = unwaited_barriers(body)
+        assert len(barriers) >= 2 and not bad, (m.group(1), len(barriers), bad)
+        # the check sees a wait that is missing, at either barrier of the loop
+        waits = [w for w in re.finditer(r"\bvmcnt\(0\)", body)]
+        assert waits
+        for w in waits:
+            without = body[:w.start()] + "vmcnt(5)" + body[w.end():]
+            before = body[:w.start()].count("\n")
+            if re.search(r"^\s*s_barrier", "\n".join(body.splitlines()[before:before + 4]), re.M):
+                assert unwaited_barriers(without)[1], (m.group(1), before)
+        found += 1
+    assert found == 6
+
+
+def test_the_products_ask_for_the_wait_themselves():
+    """Whatever the compiler makes of a barrier: no bare one stands in the source of the staged loop."""
+    source = open(B.HEAD_SRC).read()
+    tile = source[source.index("struct Tile {"):source.index("// Which tile and split")]
+    assert tile.count("meet();") == 2 and "__syncthreads" not in tile
+    assert re.search(r"void meet\(\) \{\s*__builtin_amdgcn_s_waitcnt\(0x0F70\);[^\n]*\n\s*__syncthreads\(\);", source)
