@@ -666,8 +666,10 @@ int zero_layernorm_grad(const zero_rows* x, const zero_rows* y_grad, const void*
 
 /* Bytes of the workspace (256-byte aligned) of zero_loss_head (gradients = 0)
  * and zero_loss_head_grad (gradients = 1) for up to n_tokens tokens, whatever
- * the strides; 0 if a size is out of range.  It does not grow with n_tokens
- * past some thousands: scores exist for one block of tokens at a time. */
+ * the strides; 0 if a size is out of range.  Scores exist for one block of
+ * tokens at a time, and the size does not grow with n_tokens past a block: as
+ * many tokens as have 256 MiB of 16-bit scores or 1 GiB of hidden rows at 8
+ * bytes an element, whichever are fewer, but 256 at least. */
 size_t zero_loss_head_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t cols, int32_t gradients);
 
 /* Device.  Scores z = x·tableᵀ of x->rows tokens over table->rows words, and

@@ -509,6 +509,11 @@ constexpr int64_t kMostVocab = int64_t(1) << 22, kMostCols = int64_t(1) << 16;  
 // The codes of a block of tokens: as many as fit the 256 MB last-level cache
 // (larger blocks were not measured against it).
 constexpr int64_t kCodeBytes = int64_t(1) << 28;
+// What a block holds for each element of its hidden rows: copies on 16-byte
+// lines and turned, 2 bytes each, and 4 of the sums before they are rounded.
+// Over a small vocabulary these are what grows with a block, not the codes:
+// 1 GiB for them, 26,112 tokens at 5120 columns.
+constexpr int64_t kRowBytes = int64_t(1) << 30;
 constexpr int64_t kCus = 256, kMostParts = 512;
 
 constexpr int64_t round_up(int64_t n, int64_t to) { return ceil_div(n, to) * to; }
@@ -539,7 +544,8 @@ Space space_of(int64_t tokens, int64_t vocab, int64_t cols, bool gradients) {
   s.k = round_up(cols, kStep);
   s.vocab_padded = round_up(vocab, kTileN);
   s.n_pieces = ceil_div(vocab, kPiece);
-  const int64_t most = std::max<int64_t>(kCodeBytes / (2 * s.vocab_padded) / kTileM, 1) * kTileM;
+  const int64_t fit = std::min(kCodeBytes / (2 * s.vocab_padded), kRowBytes / (8 * s.k));
+  const int64_t most = std::max<int64_t>(fit / kTileM, 1) * kTileM;
   s.block = std::min(most, std::max<int64_t>(round_up(tokens, kTileM), kTileM));
   s.part_stride = round_up(cols, 8);
   size_t at = 0;

@@ -251,3 +251,19 @@ def test_an_embedding_without_max_tokens_refuses_gradients(tokens):
     op._on = lambda *tensors: None  # the tensors stand for ones on the operator's GPU
     with pytest.raises(ValueError, match="max_tokens"):
         op.grad(torch.zeros(tokens, dtype=torch.int64), torch.zeros(tokens, 8), table)
+
+
+@pytest.mark.parametrize("vocab", [1, 300, 500, 4099, 50257])
+@pytest.mark.parametrize("cols", [1, 64, 4096, 5120, 16384, 1 << 16])
+def test_loss_head_workspace_is_bounded_whatever_the_tokens(vocab, cols):
+    """A block of tokens is what it holds, so past a block it stays as it is, over small vocabularies too.  The bound
+    adds up a block's parts at their most: codes and their turned copy (2^28 bytes each, or 256 tokens of them), 8 bytes
+    an element of its hidden rows (2^30, or 256 tokens of them), the same again for parts of sums that are split (2^27)
+    and small statistics (2^26), and the table's copies and sums (2 + 2 + 4 bytes an element)."""
+    wide, words = -(-cols // 64) * 64, -(-vocab // 256) * 256
+    codes, rows = max(1 << 28, 512 * words), max(1 << 30, 256 * 8 * wide)
+    for gradients in (False, True):
+        sizes = [Z.zero_loss_head_workspace_bytes(t, vocab, cols, gradients) for t in
+                 (1, 256, 4096, 65536, 1 << 18, 1 << 20, 1 << 24, 2**31 - 1)]
+        assert sizes == sorted(sizes) and sizes[-3] == sizes[-1], sizes
+        assert sizes[-1] <= 2 * codes + rows + (1 << 27) + (1 << 26) + 8 * words * wide, sizes

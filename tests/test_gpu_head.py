@@ -214,3 +214,14 @@ def test_gradients_against_differences():
                 found.append(loss(*moved))
             want = (found[0] - found[1]) / (2 * step)
             assert abs(grad.reshape(-1)[i].item() - want) <= 2.0**-8 * grad.abs().max().item(), (k, i)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_more_tokens_than_one_block_holds_over_a_small_vocabulary(accumulate):
+    """Rows of 16384 columns leave blocks of 8192 tokens whatever the vocabulary: two of them, the second ragged."""
+    h = Head(8192 + 259, 40, 16384, "bf16", ignored=0.1, sigma=5e-4).want(2.0)
+    op = LossHead(h.table, max_tokens=8192 + 259)
+    op.ws.fill_(0xFF)
+    op.grad(h.x, h.labels, h.losses, h.loss, h.count, h.dx, h.dw, accumulate=accumulate, scale=2.0)
+    h.check_losses()
+    h.check_grads(accumulate)
