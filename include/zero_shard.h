@@ -679,7 +679,8 @@ size_t zero_loss_head_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t c
  * gradients zeros.  Where none counts, *loss is 0.  x and table: the same
  * 16-bit format and cols (fp32 is refused: the products take 16-bit factors).
  * label_bytes: 4 (int32) or 8 (int64).  losses_dev (x->rows), loss_dev: fp32.
- * Scores are sums in fp32, never rounded to fewer bits for the losses.  A
+ * Scores are sums in fp32, never rounded to fewer bits for the losses, and the
+ * loss of a token that is all but sure of its label keeps its digits.  A
  * score that is NaN or +inf makes its token's loss (and gradients) NaN; one of
  * -inf is a word of probability 0.  table->rows in [1, 2^22], cols at most
  * 2^16. */

@@ -13,6 +13,11 @@
 // 2^-12 octaves (1.7e-4 of the exponential), finer than the rounding that the
 // factor of the other two products needs, so the scores are computed once and
 // never held in 32 bits.  softmax_kernel turns the codes into G, rounded once.
+// The label's word is left out of maxima and sums: with R the logarithm of the
+// sum over the others, loss_t = log(1 + exp(R - z_t,label)), which keeps its
+// digits where the label is all but certain, and so does expm1(-loss_t), the
+// label's factor in G.  Taken as lse_t - z_t,label both would end at the last
+// digit of a score (1e-6 at a score of 20).
 //
 // Measured (calls behind one another): 4096 tokens x 50257 words x 1600 columns
 // bf16 2.58 ms, 4096 x 32000 x 4096 fp16 3.04 ms, of which the three products
@@ -197,7 +202,8 @@ struct Block {             // a block of tokens
 };
 
 // The scores of a tile into codes (nullptr: none), and for each row and piece
-// the maximum and the sum of 2^(score - maximum); all in octaves.
+// the maximum and the sum of 2^(score - maximum) over the words that are not
+// the token's label; all in octaves.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void scores_kernel(Product p, Block blk, int64_t vocab,
                                                           const void* __restrict__ labels, int label_bytes,
@@ -212,15 +218,22 @@ __global__ __launch_bounds__(kThreads) void scores_kernel(Product p, Block blk, 
 #pragma unroll
   for (int i = 0; i < kBlocksM; ++i) {
     const int m = w.m * kTileM + t.m(i);
+    const uint32_t label = m < blk.tokens ? local_row(labels, label_bytes, blk.first + m, 0, vocab) : kNoRow;
     float z[kBlocksN][4], top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kBlocksN; ++j)
+    for (int j = 0; j < kBlocksN; ++j) {
+      const int n = w.n * kTileN + t.n(j);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const bool some = w.n * kTileN + t.n(j) + q < vocab;
-        z[j][q] = some ? t.acc[i][j][q] * kLog2e : -INFINITY;
-        top = fmaxf(top, z[j][q]);
+      for (int q = 0; q < 4; ++q) z[j][q] = n + q < vocab ? t.acc[i][j][q] * kLog2e : -INFINITY;
+      const uint32_t q_label = label - static_cast<uint32_t>(n);
+      if (q_label < 4) {
+        label_score[m] = q_label == 0 ? z[j][0] : q_label == 1 ? z[j][1] : q_label == 2 ? z[j][2] : z[j][3];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) z[j][q] = q_label == q ? -INFINITY : z[j][q];
       }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) top = fmaxf(top, z[j][q]);
+    }
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const float base = top == -INFINITY ? 0.0f : top;  // nothing but -inf: the sum is 0
@@ -233,17 +246,13 @@ __global__ __launch_bounds__(kThreads) void scores_kernel(Product p, Block blk, 
     sum += __shfl_xor(sum, 32, 64);
     if (m >= blk.tokens) continue;
     if (group == 0 && n_wave < vocab) pieces[static_cast<int64_t>(m) * n_pieces + n_wave / kPiece] = make_float2(top, sum);
-    const uint32_t label = local_row(labels, label_bytes, blk.first + m, 0, vocab);
+    if (codes) {
 #pragma unroll
-    for (int j = 0; j < kBlocksN; ++j) {
-      const int n = w.n * kTileN + t.n(j);
-      const uint32_t q_label = label - static_cast<uint32_t>(n);
-      if (q_label < 4) label_score[m] = q_label == 0 ? z[j][0] : q_label == 1 ? z[j][1] : q_label == 2 ? z[j][2] : z[j][3];
-      if (codes) {
+      for (int j = 0; j < kBlocksN; ++j) {
         uint32_t c[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) c[q] = static_cast<uint32_t>(fminf((base - z[j][q]) * kCodeSteps + 0.5f, 65535.0f));
-        *reinterpret_cast<u32x2*>(codes + m * code_stride + n) = u32x2{c[0] | c[1] << 16, c[2] | c[3] << 16};
+        *reinterpret_cast<u32x2*>(codes + m * code_stride + w.n * kTileN + t.n(j)) = u32x2{c[0] | c[1] << 16, c[2] | c[3] << 16};
       }
     }
   }
@@ -273,10 +282,18 @@ __global__ __launch_bounds__(kBlock) void lse_kernel(Block blk, int64_t vocab, c
     top = higher;
   }
   if (lane == 0) {
-    const float l = top + __builtin_amdgcn_logf(sum);
-    lse[m] = l;
     const bool counts = local_row(labels, label_bytes, blk.first + m, 0, vocab) != kNoRow;
-    losses[blk.first + m] = counts ? (l - label_score[m]) * kLn2 : 0.0f;
+    float loss = 0.0f, l = 0.0f;  // l is not read for a token that does not count
+    if (counts) {
+      const float rest = top + __builtin_amdgcn_logf(sum), own = label_score[m], above = rest - own;
+      const float more = log1pf(__builtin_amdgcn_exp2f(-fabsf(above)));  // what the smaller of the two adds to the larger
+      loss = fmaxf(above, 0.0f) * kLn2 + more;
+      l = fmaxf(rest, own) + more * kLog2e;
+      // fmaxf passes over a NaN, and above is -inf for an own score of +inf
+      if (above != above || own == INFINITY) loss = l = __builtin_nanf("");
+    }
+    lse[m] = l;
+    losses[blk.first + m] = loss;
   }
 }
 
@@ -290,7 +307,7 @@ template <int DT>
 __global__ __launch_bounds__(kBlock) void softmax_kernel(Block blk, int64_t vocab, const void* __restrict__ labels,
                                                          int label_bytes, uint16_t* __restrict__ codes,
                                                          int64_t code_stride, const float2* __restrict__ pieces,
-                                                         int64_t n_pieces, const float* __restrict__ label_score,
+                                                         int64_t n_pieces, const float* __restrict__ losses,
                                                          const float* __restrict__ lse, uint16_t* __restrict__ turned,
                                                          int64_t turned_stride) {
   __shared__ uint16_t tile[64][64 + 2];
@@ -310,7 +327,7 @@ __global__ __launch_bounds__(kBlock) void softmax_kernel(Block blk, int64_t voca
       for (int i = 0; i < 8; ++i) {
         const uint32_t code = i & 1 ? q[i / 2] >> 16 : q[i / 2] & 0xFFFFu;
         float p = code == kNoCode ? l - l : __builtin_amdgcn_exp2f(base - static_cast<float>(code) * (1.0f / kCodeSteps));
-        if (n0 + c + i == label) p = expm1f((label_score[m] - l) * kLn2);
+        if (n0 + c + i == label) p = expm1f(-losses[blk.first + m]);
         if (n0 + c + i >= vocab) p = 0.0f;
         g.set(i, DT == ZERO_FP16 ? p * kHalfScale : p);
       }
@@ -703,7 +720,7 @@ int run(const Call& c, bool gradients) {
     }
     if (!gradients) continue;
     LAUNCH((softmax_kernel<DT>), dim3(s.vocab_padded / 64, blk.padded / 64), kBlock, blk, vocab, c.labels, c.label_bytes,
-           codes, s.vocab_padded, pieces, s.n_pieces, label_score, lse, turned, static_cast<int64_t>(blk.padded));
+           codes, s.vocab_padded, pieces, s.n_pieces, c.losses, lse, turned, static_cast<int64_t>(blk.padded));
     LAUNCH((turn_kernel<DT>), dim3(blk.padded / 64, ceil_div(cols, 64)), kBlock, device_rows(&here), c.labels,
            c.label_bytes, first, vocab, x_turned, static_cast<int64_t>(blk.padded));
     if (blk.tokens > 0) {

@@ -225,3 +225,39 @@ def test_more_tokens_than_one_block_holds_over_a_small_vocabulary(accumulate):
     op.grad(h.x, h.labels, h.losses, h.loss, h.count, h.dx, h.dw, accumulate=accumulate, scale=2.0)
     h.check_losses()
     h.check_grads(accumulate)
+
+
+@pytest.mark.parametrize("dt", FORMATS)
+@pytest.mark.parametrize("high", [24.0, 40.0, -40.0])
+def test_tokens_that_are_sure_of_their_word(dt, high):
+    """Scores that fp32 holds exactly: `high` for the label, half of it for the 99 others (the label's loss is
+    log(1 + 99 e^(-high / 2)), 2e-7 at 40).  In octaves the two scores are off by 1.5 * 2^-24 of themselves, their
+    difference by 1.5 * 2^-24 * 1.5 * |high| log2(e) = 3.3 |high| 2^-24; the logarithm of the others' sum, its addition
+    and the difference round once at 2 |high| 2^-24 at most together, so the loss is off by less than
+    8 |high| 2^-24 of itself where it is small, and by that many octaves where it is large.  A factor is off by one
+    rounding of its format and by as much as the loss."""
+    n, vocab = 70, 100
+    dtype = FORMATS[dt]
+    x, table = (torch.zeros(k, 64, dtype=dtype, device=DEV) for k in (n, vocab))
+    x[:, 0], table[:, 0], table[9, 0] = abs(high), math.copysign(0.5, high), math.copysign(1.0, high)
+    labels = torch.full((n,), 9, device=DEV)
+    losses, loss = torch.zeros(n, device=DEV), torch.zeros(1, device=DEV)
+    count = torch.zeros(1, dtype=torch.int64, device=DEV)
+    dx, dw = torch.zeros_like(x), torch.zeros_like(table)
+    scale = 2.0**17 if high > 30 else 1.0  # keeps the gradients among the format's normal numbers
+    LossHead(table, max_tokens=n).grad(x, labels, losses, loss, count, dx, dw, scale=scale)
+    rest = math.log(99.0) - high / 2
+    want = math.log1p(math.exp(rest)) if rest < 0 else rest + math.log1p(math.exp(-rest))
+    off = 8 * abs(high) * U * max(want, 1.0 if want > 0.5 else want)
+    assert (losses.double() - want).abs().max().item() <= off
+    assert abs(loss.item() - want) <= off + 2 * U * want
+    assert count.item() == n
+    step = torch.finfo(dtype).eps / 2
+    g = -math.expm1(-want) * scale / n  # of the label, negative; the others' factors add up to it
+    rel = step + 2.0**-12 * math.log(2) + 8 * abs(high) * U
+    want_dx = -g * math.copysign(0.5, high)
+    assert (dx[:, 0].double() - want_dx).abs().max().item() <= 1.01 * abs(want_dx) * (3 * rel + step)
+    assert not dx[:, 1:].any() and not dw[:, 1:].any()
+    want_dw = torch.full((vocab,), g / 99 * n * abs(high), dtype=torch.float64, device=DEV)
+    want_dw[9] = -g * n * abs(high)
+    assert ((dw[:, 0].double() - want_dw).abs() <= 1.01 * want_dw.abs() * (rel + step)).all()
