@@ -616,8 +616,8 @@ typedef struct zero_rows {
 /* Device.  out[t] = scale · table[ids[t] - first_row], rounded to out's
  * format, for out->rows tokens; zeros where that row is not one of the
  * table's (a rank that holds a slice of the vocabulary adds up the slices'
- * outputs).  id_bytes: 4 (int32) or 8 (int64).  table and out: any formats,
- * the same cols. */
+ * outputs).  id_bytes: 4 (int32) or 8 (int64).  scale: finite in fp32, as are
+ * the other factors below and eps.  table and out: any formats, the same cols. */
 int zero_embed_forward(const zero_rows* table, int64_t first_row, const void* ids_dev, int32_t id_bytes, double scale,
                        const zero_rows* out, void* stream);
 

@@ -489,6 +489,7 @@ int zero_embed_forward(const zero_rows* table, int64_t first_row, const void* id
   if (rc != ZERO_OK) return rc;
   if (table->cols != out->cols) return fail(ZERO_ERR_INVALID, "%s: table and out differ in cols", fn);
   if (first_row < 0) return fail(ZERO_ERR_INVALID, "%s: first_row < 0", fn);
+  if (!finite32(scale)) return fail(ZERO_ERR_INVALID, "%s: scale is not finite in fp32", fn);
   if (out->rows == 0) return ZERO_OK;
   const int64_t units = ceil_div(out->cols, 8);
   // Four units a thread once that leaves workgroups for every CU; before, one token a workgroup.
@@ -519,6 +520,7 @@ int zero_embed_grad(const void* ids_dev, int32_t id_bytes, int64_t first_row, co
   if (rc != ZERO_OK) return rc;
   if (table_grad->cols != out_grad->cols) return fail(ZERO_ERR_INVALID, "%s: out_grad and table_grad differ in cols", fn);
   if (first_row < 0) return fail(ZERO_ERR_INVALID, "%s: first_row < 0", fn);
+  if (!finite32(scale)) return fail(ZERO_ERR_INVALID, "%s: scale is not finite in fp32", fn);
   const int64_t tokens = out_grad->rows, rows = table_grad->rows, cols = out_grad->cols;
   const EmbedSpace w = embed_space(tokens, rows, cols);
   if (!ws_dev || !aligned16(ws_dev) || ws_bytes < w.bytes)

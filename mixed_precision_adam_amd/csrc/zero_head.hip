@@ -659,7 +659,7 @@ int check(const Call& c, bool gradients) {
       if (g->rows != of->rows || g->cols != of->cols || g->dt != of->dt)
         return fail(ZERO_ERR_INVALID, "%s: %s has another shape or dtype than what it is of", fn, name);
     }
-    if (!std::isfinite(c.scale)) return fail(ZERO_ERR_INVALID, "%s: scale is not finite", fn);
+    if (!finite32(c.scale)) return fail(ZERO_ERR_INVALID, "%s: scale is not finite in fp32", fn);
     if (!aligned8(c.state)) return fail(ZERO_ERR_INVALID, "%s: misaligned step state", fn);
   }
   const Space s = space_of(c.x->rows, c.table->rows, c.x->cols, gradients);

@@ -343,7 +343,7 @@ int zero_layernorm_forward(const zero_rows* x, const void* weight_dev, const voi
   if (rc == ZERO_OK) rc = same_shape(fn, "y", y, x);
   if (rc == ZERO_OK) rc = weight_ok(fn, weight_dev, bias_dev, wdt, x);
   if (rc != ZERO_OK) return rc;
-  if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(ZERO_ERR_INVALID, "%s: eps out of range", fn);
+  if (!(eps >= 0.0) || !finite32(eps)) return fail(ZERO_ERR_INVALID, "%s: eps out of range", fn);
   if (unaligned(mean_dev, 4) || unaligned(rstd_dev, 4)) return fail(ZERO_ERR_INVALID, "%s: misaligned statistics", fn);
   if (x->rows == 0) return ZERO_OK;
   return with_dtype(x->dt, [&](auto dt) {

@@ -4,6 +4,7 @@
 #define ZERO_UNITS_H
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "zero_common.h"
@@ -215,6 +216,10 @@ inline int ids_ok(const char* fn, const void* ids, int32_t id_bytes, int64_t n) 
   if (unaligned(ids, static_cast<uintptr_t>(id_bytes))) return fail(ZERO_ERR_INVALID, "%s: ids misaligned", fn);
   return ZERO_OK;
 }
+
+// Whether a factor that kernels take in fp32 is finite there: a larger one would
+// make NaN of what has to stay zero.
+inline bool finite32(double f) { return std::isfinite(static_cast<float>(f)); }
 
 }  // namespace zero_detail
 

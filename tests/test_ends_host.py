@@ -267,3 +267,14 @@ def test_loss_head_workspace_is_bounded_whatever_the_tokens(vocab, cols):
                  (1, 256, 4096, 65536, 1 << 18, 1 << 20, 1 << 24, 2**31 - 1)]
         assert sizes == sorted(sizes) and sizes[-3] == sizes[-1], sizes
         assert sizes[-1] <= 2 * codes + rows + (1 << 27) + (1 << 26) + 8 * words * wide, sizes
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF, 1e39, -1e39])
+def test_factors_that_fp32_does_not_hold_are_refused(bad):
+    """Times infinity, the zeros of a token outside the table and of a word without gradient would become NaN."""
+    a, b = rows(), rows(3)
+    refused(LIB.zero_embed_forward(a, 0, 8, 8, bad, b, None), "scale")
+    refused(LIB.zero_embed_grad(8, 8, 0, b, bad, a, 0, 4096, Z.zero_embed_grad_workspace_bytes(3, 4, 8), None), "scale")
+    refused(LIB.zero_loss_head_grad(b, a, 8, 8, bad, None, 4096, 4096, 4096, b, a, 0, 4096,
+                                    Z.zero_loss_head_workspace_bytes(3, 4, 8), None), "scale")
+    refused(LIB.zero_layernorm_forward(a, 16, None, 0, bad, 1, a, None, None, None), "eps")
