@@ -672,6 +672,12 @@ int zero_layernorm_grad(const zero_rows* x, const zero_rows* y_grad, const void*
  * bytes an element, whichever are fewer, but 256 at least. */
 size_t zero_loss_head_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t cols, int32_t gradients);
 
+/* The same for calls with this table alone (its place, stride and format; 0
+ * where the calls would refuse it).  Less by a copy of the table where its
+ * rows can be read where they are: cols a multiple of 64, stride of 8 and below
+ * 2^22, data on a 16-byte line. */
+size_t zero_loss_head_workspace_bytes_for(int64_t n_tokens, const zero_rows* table, int32_t gradients);
+
 /* Device.  Scores z = x·tableᵀ of x->rows tokens over table->rows words, and
  *   losses[t] = log(sum of exp(z[t])) - z[t][labels[t]]
  *   *loss     = sum of losses / count,  *count = number of tokens that count

@@ -177,6 +177,8 @@ _lib.zero_layernorm_grad.argtypes = [_ROWS, _ROWS, _P, C.c_int32, C.c_int32, _P,
                                      C.c_int32, _P, C.c_size_t, _P]
 _lib.zero_loss_head_workspace_bytes.argtypes = [C.c_int64, C.c_int64, C.c_int64, C.c_int32]
 _lib.zero_loss_head_workspace_bytes.restype = C.c_size_t
+_lib.zero_loss_head_workspace_bytes_for.argtypes = [C.c_int64, _ROWS, C.c_int32]
+_lib.zero_loss_head_workspace_bytes_for.restype = C.c_size_t
 _lib.zero_loss_head.argtypes = [_ROWS, _ROWS, _P, C.c_int32, _P, _P, _P, _P, C.c_size_t, _P]
 _lib.zero_loss_head_grad.argtypes = [_ROWS, _ROWS, _P, C.c_int32, C.c_double, _P, _P, _P, _P, _ROWS, _ROWS, C.c_int32,
                                      _P, C.c_size_t, _P]
@@ -194,7 +196,8 @@ EXPORTS = ("zero_last_error", "zero_shard_layout", "zero_flatten_plan", "zero_bu
            "zero_list_adamw_step_dev", "zero_list_adamw8_step_dev", "zero_list_state8_pack",
            "zero_list_state8_unpack", "zero_embed_forward", "zero_embed_grad_workspace_bytes", "zero_embed_grad",
            "zero_layernorm_forward", "zero_layernorm_grad_workspace_bytes", "zero_layernorm_grad",
-           "zero_loss_head_workspace_bytes", "zero_loss_head", "zero_loss_head_grad")
+           "zero_loss_head_workspace_bytes", "zero_loss_head_workspace_bytes_for", "zero_loss_head",
+           "zero_loss_head_grad")
 ZERO_STEP_ERR_LOSS_SCALE = 1  # zero_step_state.error: the decision could not be taken
 ZERO_NOALLOC_SCRATCH_BYTES = 6 << 20  # static scratch of zero_flatten_grads_sqnorm_noalloc, per device
 
@@ -661,6 +664,10 @@ def zero_layernorm_grad(x, y_grad, weight, mean, rstd, x_grad, weight_grad, bias
 
 def zero_loss_head_workspace_bytes(n_tokens: int, vocab: int, cols: int, gradients: bool = True) -> int:
     return int(_lib.zero_loss_head_workspace_bytes(n_tokens, vocab, cols, int(gradients)))
+
+
+def zero_loss_head_workspace_bytes_for(n_tokens: int, table, gradients: bool = True) -> int:
+    return int(_lib.zero_loss_head_workspace_bytes_for(n_tokens, _rows(table, "table"), int(gradients)))
 
 
 def _scalar(x, dtype, name: str):

@@ -556,7 +556,9 @@ int split_count(int64_t tiles, int64_t steps) {
   return best;
 }
 
-Space space_of(int64_t tokens, int64_t vocab, int64_t cols, bool gradients) {
+// With or without room for the table's rows on 16-byte lines, which comes last: a
+// call whose table is read where it is fits a workspace made without it.
+Space space_of(int64_t tokens, int64_t vocab, int64_t cols, bool gradients, bool table_copy) {
   Space s{};
   s.k = round_up(cols, kStep);
   s.vocab_padded = round_up(vocab, kTileN);
@@ -576,7 +578,6 @@ Space space_of(int64_t tokens, int64_t vocab, int64_t cols, bool gradients) {
   s.lse = part(4 * s.block);
   s.pieces = part(8 * s.block * s.n_pieces);
   s.x = part(2 * s.block * s.k);
-  s.table = part(2 * vocab * s.k);
   if (gradients) {
     s.codes = part(2 * s.block * s.vocab_padded);
     s.turned = part(2 * s.block * s.vocab_padded);
@@ -591,6 +592,7 @@ Space space_of(int64_t tokens, int64_t vocab, int64_t cols, bool gradients) {
     s.parts = part(4 * rows * s.part_stride);
     s.sums = part(tokens > s.block ? 4 * vocab * s.part_stride : 0);
   }
+  s.table = part(table_copy ? 2 * vocab * s.k : 0);
   s.bytes = at;
   return s;
 }
@@ -662,7 +664,7 @@ int check(const Call& c, bool gradients) {
     if (!finite32(c.scale)) return fail(ZERO_ERR_INVALID, "%s: scale is not finite in fp32", fn);
     if (!aligned8(c.state)) return fail(ZERO_ERR_INVALID, "%s: misaligned step state", fn);
   }
-  const Space s = space_of(c.x->rows, c.table->rows, c.x->cols, gradients);
+  const Space s = space_of(c.x->rows, c.table->rows, c.x->cols, gradients, !direct(c.table));
   if (!c.ws || (reinterpret_cast<uintptr_t>(c.ws) & 255) != 0 || c.ws_bytes < s.bytes)
     return fail(ZERO_ERR_INVALID, "%s: workspace of %zu bytes, %zu needed, 256-byte aligned", fn, c.ws ? c.ws_bytes : 0,
                 s.bytes);
@@ -675,7 +677,7 @@ int check(const Call& c, bool gradients) {
 template <int DT>
 int run(const Call& c, bool gradients) {
   const int64_t tokens = c.x->rows, vocab = c.table->rows, cols = c.x->cols;
-  const Space s = space_of(tokens, vocab, cols, gradients);
+  const Space s = space_of(tokens, vocab, cols, gradients, !direct(c.table));
   char* ws = static_cast<char*>(c.ws);
   float* factor = reinterpret_cast<float*>(ws + s.factor);
   float* label_score = reinterpret_cast<float*>(ws + s.label_score);
@@ -755,7 +757,14 @@ extern "C" {
 
 size_t zero_loss_head_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t cols, int32_t gradients) {
   if (!head_sizes_ok(n_tokens, vocab, cols)) return 0;
-  return space_of(n_tokens, vocab, cols, gradients != 0).bytes;
+  return space_of(n_tokens, vocab, cols, gradients != 0, true).bytes;
+}
+
+size_t zero_loss_head_workspace_bytes_for(int64_t n_tokens, const zero_rows* table, int32_t gradients) {
+  if (rows_ok("zero_loss_head_workspace_bytes_for", "table", table) != ZERO_OK || !dtype_ok(table->dt) ||
+      !head_sizes_ok(n_tokens, table->rows, table->cols))
+    return 0;
+  return space_of(n_tokens, table->rows, table->cols, gradients != 0, !direct(table)).bytes;
 }
 
 int zero_loss_head(const zero_rows* x, const zero_rows* table, const void* labels_dev, int32_t label_bytes,

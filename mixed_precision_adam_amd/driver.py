@@ -29,9 +29,9 @@ from . import (ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO_LIST_HAS_PARAMS, ZERO_LIST_
                zero_list_adamw_step, zero_list_adamw_step_dev, zero_list_decision_dev, zero_list_grad_sqnorm,
                zero_list_grad_sqnorm_workspace_bytes, zero_list_plan, zero_list_repoint, zero_list_state8_pack,
                zero_list_state8_unpack, zero_list_tensor, zero_loss_head, zero_loss_head_grad,
-               zero_loss_head_workspace_bytes, zero_shard_layout, zero_sqnorm_reduce, zero_state8_bytes,
-               zero_state_tile, zero_state_tiled_numel, zero_state_untile, zero_step_decision, zero_step_decision_dev,
-               zero_step_state_init)
+               zero_loss_head_workspace_bytes, zero_loss_head_workspace_bytes_for, zero_shard_layout,
+               zero_sqnorm_reduce, zero_state8_bytes, zero_state_tile, zero_state_tiled_numel, zero_state_untile,
+               zero_step_decision, zero_step_decision_dev, zero_step_state_init)
 
 _FORMAT = {torch.bfloat16: ZERO_BF16, torch.float16: ZERO_FP16, torch.float32: ZERO_FP32}
 _ADDRESS = (int, type(None))  # what a call takes in place of a tensor
@@ -600,9 +600,11 @@ class LossHead(_Operator):
     def __init__(self, table, *, max_tokens: int, gradients: bool = True, workspace=None):
         self.table, self.max_tokens, self.gradients = table, max_tokens, bool(gradients)
         self.device = table.device
-        need = zero_loss_head_workspace_bytes(max_tokens, *table.shape, gradients)
-        if need == 0:
+        if zero_loss_head_workspace_bytes(max_tokens, *table.shape, gradients) == 0:
             raise ValueError(f"{max_tokens} tokens over a table of {tuple(table.shape)}: out of range")
+        need = zero_loss_head_workspace_bytes_for(max_tokens, table, gradients)
+        if need == 0:
+            raise ValueError(f"a table of 16-bit elements is required, got {table.dtype}, strides {table.stride()}")
         self._workspace(need, workspace)
 
     def _fits(self, x) -> None:

@@ -278,3 +278,26 @@ def test_factors_that_fp32_does_not_hold_are_refused(bad):
     refused(LIB.zero_loss_head_grad(b, a, 8, 8, bad, None, 4096, 4096, 4096, b, a, 0, 4096,
                                     Z.zero_loss_head_workspace_bytes(3, 4, 8), None), "scale")
     refused(LIB.zero_layernorm_forward(a, 16, None, 0, bad, 1, a, None, None, None), "eps")
+
+
+def test_the_head_asks_for_a_copy_of_the_table_only_where_it_makes_one():
+    need = Z.zero_loss_head_workspace_bytes_for
+    for n in (0, 1, 33, 4096, 1 << 20):
+        for gradients in (False, True):
+            for v, d in ((50257, 1600), (32000, 4096), (300, 64)):
+                most = Z.zero_loss_head_workspace_bytes(n, v, d, gradients)
+                copy = -(-2 * v * d // 256) * 256
+                for dt in (Z.ZERO_BF16, Z.ZERO_FP16):
+                    assert need(n, rows(v, d, dt=dt), gradients) == most - copy
+                    assert need(n, rows(v, d, d + 8, dt), gradients) == most - copy
+                assert need(n, rows(v, d, d + 4), gradients) == most  # rows off the 16-byte lines
+                assert need(n, rows(v, d, data=4096 + 8), gradients) == most
+                assert need(n, rows(v, d, 1 << 22), gradients) == most
+            assert need(n, rows(300, 65), gradients) == Z.zero_loss_head_workspace_bytes(n, 300, 65, gradients)
+    assert need(4, rows(300, 64, dt=Z.ZERO_FP32)) == need(-1, rows(300, 64)) == need(4, rows(0, 64, data=None)) == 0
+    # a call takes what was asked for, for its table and for as many tokens, and no less
+    x, w = rows(4, 64), rows(11, 64)
+    refused(LIB.zero_loss_head(x, w, 8, 8, 4096, 4096, 4096, 4096, need(4, w, False) - 1, None), "workspace")
+    refused(LIB.zero_loss_head(x, rows(11, 64, 65), 8, 8, 4096, 4096, 4096, 4096, need(4, w, False), None), "workspace")
+    refused(LIB.zero_loss_head_grad(x, w, 8, 8, 1.0, None, 4096, 4096, 4096, x, w, 0, 4096, need(4, w) - 1, None),
+            "workspace")

@@ -261,3 +261,25 @@ def test_tokens_that_are_sure_of_their_word(dt, high):
     want_dw = torch.full((vocab,), g / 99 * n * abs(high), dtype=torch.float64, device=DEV)
     want_dw[9] = -g * n * abs(high)
     assert ((dw[:, 0].double() - want_dw).abs() <= 1.01 * want_dw.abs() * (rel + step)).all()
+
+
+@pytest.mark.parametrize("gradients", [False, True])
+@pytest.mark.parametrize("tokens,vocab,cols,spare", [(33, 300, 64, 0), (300, 777, 192, 8), (300, 777, 192, 3)])
+def test_a_table_read_where_it_is_needs_no_room_for_a_copy(tokens, vocab, cols, spare, gradients):
+    """The operator's workspace is what its table needs, and what lies behind it is left alone."""
+    h = Head(tokens, vocab, cols, "bf16", spare).want()
+    need = Z.zero_loss_head_workspace_bytes_for(tokens, h.table, gradients)
+    copy = 0 if spare % 8 else -(-2 * vocab * cols // 256) * 256
+    assert need == Z.zero_loss_head_workspace_bytes(tokens, vocab, cols, gradients) - copy
+    assert LossHead(h.table, max_tokens=tokens, gradients=gradients).ws.numel() == need
+    room = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+    op = LossHead(h.table, max_tokens=tokens, gradients=gradients, workspace=room)
+    if gradients:
+        op.grad(h.x, h.labels, h.losses, h.loss, h.count, h.dx, h.dw)
+        h.check_grads(False)
+    else:
+        op.forward(h.x, h.labels, h.losses, h.loss, h.count)
+    h.check_losses()
+    assert (room[need:] == 0xFF).all()
+    with pytest.raises(ValueError, match="16-bit"):
+        LossHead(h.table.float(), max_tokens=tokens)
