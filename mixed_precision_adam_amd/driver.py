@@ -506,6 +506,8 @@ class _Operator:
     It keeps its tensors and its workspace alive: keep it until its calls are done, and give calls that may overlap in
     time (two streams, two captured graphs) operators of their own."""
 
+    ws, ws_bytes = None, 0
+
     def _on(self, *tensors) -> None:
         at = self.device.index
         for t in tensors:
@@ -566,17 +568,20 @@ class TokenEmbedding(_Operator):
 
 
 class LayerNorm(_Operator):
-    """Layer norm over the rows of a matrix (`mean=False`: without subtracting the mean), and its gradients.  Norms
-    whose calls do not overlap in time may share a workspace (`workspace=other.ws`)."""
+    """Layer norm over the rows of a matrix (`mean=False`: without subtracting the mean), and its gradients.  Their
+    workspace takes 4 KiB a column, 16 in rows of up to 1024: norms whose calls do not overlap in time may share one
+    (`workspace=other.ws`), and with `gradients=False`, for the forward pass alone, there is none."""
 
-    def __init__(self, weight, bias=None, *, eps: float = 1e-5, mean: bool = True, workspace=None):
+    def __init__(self, weight, bias=None, *, eps: float = 1e-5, mean: bool = True, gradients: bool = True,
+                 workspace=None):
         self.weight, self.bias, self.eps, self.mean = weight, bias, float(eps), bool(mean)
-        self.device = weight.device
+        self.gradients, self.device = bool(gradients), weight.device
         self._on(bias)
         need = zero_layernorm_grad_workspace_bytes(2**31 - 1, weight.numel())  # enough for any number of rows
         if need == 0:
             raise ValueError(f"rows of {weight.numel()} elements: out of range")
-        self._workspace(need, workspace)
+        if gradients:
+            self._workspace(need, workspace)
 
     def forward(self, x, out, mean=None, rstd=None, stream=None) -> None:
         """The statistics of each row are left in `mean` and `rstd` (fp32) where these are given."""
@@ -587,6 +592,8 @@ class LayerNorm(_Operator):
     def grad(self, x, out_grad, mean, rstd, x_grad=None, weight_grad=None, bias_grad=None, accumulate: bool = False,
              stream=None) -> None:
         """Those gradients that are given a place; `accumulate`: the weight's and the bias's are added to theirs."""
+        if not self.gradients:
+            raise ValueError("made without gradients")
         self._on(x, out_grad, mean, rstd, x_grad, weight_grad, bias_grad)
         self._call(zero_layernorm_grad, x, out_grad, self.weight, mean, rstd, x_grad, weight_grad, bias_grad, self.ws,
                    self.ws_bytes, center=self.mean, accumulate=accumulate, stream=stream)

@@ -301,3 +301,16 @@ def test_the_head_asks_for_a_copy_of_the_table_only_where_it_makes_one():
     refused(LIB.zero_loss_head(x, rows(11, 64, 65), 8, 8, 4096, 4096, 4096, 4096, need(4, w, False), None), "workspace")
     refused(LIB.zero_loss_head_grad(x, w, 8, 8, 1.0, None, 4096, 4096, 4096, x, w, 0, 4096, need(4, w) - 1, None),
             "workspace")
+
+
+def test_a_norm_without_gradients_holds_no_workspace():
+    op = driver.LayerNorm(torch.ones(5120), gradients=False)
+    assert op.ws is None and op.ws_bytes == 0
+    with pytest.raises(ValueError, match="without gradients"):
+        op.grad(torch.zeros(3, 5120), torch.zeros(3, 5120), torch.zeros(3), torch.zeros(3))
+    with pytest.raises(ValueError, match="out of range"):
+        driver.LayerNorm(torch.zeros(16385), gradients=False)
+    assert driver.TokenEmbedding(torch.zeros(4, 8)).ws is None
+    # what a norm with gradients holds, as its documentation says
+    for cols, each in ((64, 16384), (1024, 16384), (1600, 4096), (16384, 4096)):
+        assert Z.zero_layernorm_grad_workspace_bytes(2**31 - 1, cols) == each * cols

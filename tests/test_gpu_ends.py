@@ -269,3 +269,19 @@ def test_layernorm_grad_against_differences():
                     found.append(loss(*moved, mean))
                 want = (found[0] - found[1]) / (2 * step)
                 assert abs(grad.view(-1)[i].item() - want) <= 1e-4 * (1 + abs(want)), (mean, k, i)
+
+
+@pytest.mark.parametrize("mean", [True, False])
+def test_layernorm_without_gradients(mean):
+    """The forward pass alone needs no workspace, and gives the same bits."""
+    _, x, weight, bias = norm_inputs(33, 1600, torch.bfloat16, False, mean, 0, 0)
+    outs = []
+    for gradients in (True, False):
+        out, mu, rstd = torch.empty_like(x), torch.zeros(33, device=DEV), torch.zeros(33, device=DEV)
+        op = LayerNorm(weight, bias, mean=mean, gradients=gradients)
+        assert (op.ws is None) == (not gradients)
+        op.forward(x, out, mu, rstd)
+        outs.append((out, mu, rstd))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    with pytest.raises(ValueError, match="without gradients"):
+        op.grad(x, x, mu, rstd, torch.empty_like(x))
