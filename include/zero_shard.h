@@ -598,7 +598,9 @@ int zero_list_state8_unpack(const zero_list* from8, const zero_list* to32, void*
  * format, and every sum has one order: the same arguments give the same bits.
  * Calls are made with the device that holds the buffers current.  A workspace
  * belongs to one call at a time; what it holds between calls is of no
- * meaning, so it needs no initial value. */
+ * meaning, so it needs no initial value.  What a call writes overlaps nothing
+ * else of it, but that y may be x, and x_grad x or y_grad, the same rows at the
+ * same place. */
 
 /* Rows in device memory: row r begins at element r·stride of data.  cols >= 1,
  * rows and cols at most 2^31 - 1, stride >= cols, rows·stride <= 2^40.  data

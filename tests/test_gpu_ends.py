@@ -285,3 +285,23 @@ def test_layernorm_without_gradients(mean):
     assert all(torch.equal(a, b) for a, b in zip(*outs))
     with pytest.raises(ValueError, match="without gradients"):
         op.grad(x, x, mu, rstd, torch.empty_like(x))
+
+
+@pytest.mark.parametrize("mean", [True, False])
+@pytest.mark.parametrize("rows,cols", [(33, 1600), (5, 777), (3, 8197), (2500, 64), (130, 5120)])
+def test_layernorm_in_place(rows, cols, mean):
+    """y over x, and x_grad over x or over y_grad: the bits of a call with memory of its own for each."""
+    gen, x, weight, bias = norm_inputs(rows, cols, torch.bfloat16, False, mean, 3, 1)
+    dy, _ = matrix(rows, cols, torch.bfloat16, gen, 0.1, 5, 2)
+    op = LayerNorm(weight, bias, mean=mean)
+    out, dx = torch.empty(rows, cols, dtype=x.dtype, device=DEV), torch.empty(rows, cols, dtype=x.dtype, device=DEV)
+    mu, rstd = torch.zeros(rows, device=DEV), torch.zeros(rows, device=DEV)
+    dw, dw2 = torch.zeros(cols, device=DEV), torch.zeros(cols, device=DEV)
+    op.forward(x, out, mu, rstd)
+    op.grad(x, dy, mu, rstd, dx, dw)
+    for over in (0, 1):
+        held = [t.clone() for t in (x, dy)]
+        op.grad(*held, mu, rstd, held[over], dw2)
+        assert torch.equal(held[over], dx) and torch.equal(dw2, dw)
+    op.forward(x, x)
+    assert torch.equal(x, out)

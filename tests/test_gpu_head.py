@@ -283,3 +283,14 @@ def test_a_table_read_where_it_is_needs_no_room_for_a_copy(tokens, vocab, cols, 
     assert (room[need:] == 0xFF).all()
     with pytest.raises(ValueError, match="16-bit"):
         LossHead(h.table.float(), max_tokens=tokens)
+
+
+@pytest.mark.parametrize("tokens,vocab,cols", [(300, 777, 192), (513, (1 << 18) + 1, 24)])
+def test_hidden_rows_may_be_overwritten_by_their_gradient(tokens, vocab, cols):
+    """x_grad over x, in one block of tokens and in three: the bits of a call with memory of its own."""
+    h = Head(tokens, vocab, cols, "bf16")
+    op = LossHead(h.table, max_tokens=tokens)
+    op.grad(h.x, h.labels, h.losses, h.loss, h.count, h.dx, h.dw)
+    x, dw = h.x.clone(), torch.zeros_like(h.dw)
+    op.grad(x, h.labels, h.losses, h.loss, h.count, x, dw)
+    assert torch.equal(x, h.dx) and torch.equal(dw, h.dw)
