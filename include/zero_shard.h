@@ -633,14 +633,16 @@ size_t zero_embed_grad_workspace_bytes(int64_t n_tokens, int64_t table_rows, int
  * decide, rounded once; rows that no token names become zeros.  With
  * accumulate the sum is added to what table_grad holds, in fp32, and rows
  * that no token names are not touched.  Tokens outside the table are passed
- * over, with their out_grad unread. */
+ * over, with their out_grad unread.  Sizes whose launch would have 2^24
+ * workgroups or more are refused: rows/64 (without accumulate) and cols/512 for
+ * each of up to 512 tokens, or of the 8192 parts at most that more are split into. */
 int zero_embed_grad(const void* ids_dev, int32_t id_bytes, int64_t first_row, const zero_rows* out_grad, double scale,
                     const zero_rows* table_grad, int32_t accumulate, void* ws_dev, size_t ws_bytes, void* stream);
 
 /* Device.  Layer norm of each row of x:
  *   center = 1:  y = (x - mean)·rstd·weight + bias,  rstd = 1/sqrt(mean((x - mean)²) + eps)
  *   center = 0:  y = x·rstd·weight + bias,           rstd = 1/sqrt(mean(x²) + eps)
- * weight_dev and bias_dev (NULL: none): cols elements of format wdt, which is
+ * weight_dev, and bias_dev (NULL: none): cols elements of format wdt, which is
  * x's or ZERO_FP32.  y: x's shape and format.  mean_dev, rstd_dev: fp32 per
  * row, for the backward pass; either may be NULL (mean_dev is not written
  * where center = 0).  eps >= 0.  cols at most ZERO_LAYERNORM_MAX_COLS (a row
@@ -691,7 +693,7 @@ size_t zero_loss_head_workspace_bytes_for(int64_t n_tokens, const zero_rows* tab
  * loss of a token that is all but sure of its label keeps its digits.  A
  * score that is NaN or +inf makes its token's loss (and gradients) NaN; one of
  * -inf is a word of probability 0.  table->rows in [1, 2^22], cols at most
- * 2^16. */
+ * 2^16, rows·cols (rows rounded up to 256, cols to 64) below 2^36. */
 int zero_loss_head(const zero_rows* x, const zero_rows* table, const void* labels_dev, int32_t label_bytes,
                    float* losses_dev, float* loss_dev, int64_t* count_dev, void* ws_dev, size_t ws_bytes, void* stream);
 

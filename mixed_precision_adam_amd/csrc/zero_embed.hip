@@ -26,10 +26,12 @@ using namespace zero_detail;
 
 constexpr int64_t kMaxGroups = int64_t(1) << 20;  // workgroups of one launch; they stride over what is left
 
-// One workgroup copies `per` tokens' rows at a time, unit by unit: four units a
-// thread in flight at once.  Bound by HBM: 16384 rows of 4096 bf16 in 54 us a
-// call (5.0 TB/s; a copy between two buffers makes 4.7), 8 rows of 1600 in 7.3,
-// which is the call's host time.
+// One workgroup copies `per` tokens' rows at a time, up to four units a thread,
+// one after the other: what keeps loads in flight is the workgroups, not the
+// thread.  Bound by HBM: 16384 rows of 4096 bf16 in 50.4 us a call (5.3 TB/s of a
+// row read and one written a token; a copy between two buffers makes 4.7, here
+// frequent words' rows come from the caches), 8 rows of 1600 in 6.8, which is the
+// call's host time.
 template <int TD, int OD>
 __global__ __launch_bounds__(kBlock) void embed_forward_kernel(Rows table, int64_t first, const void* __restrict__ ids,
                                                                int id_bytes, float scale, Rows out, uint32_t per,
@@ -57,9 +59,9 @@ __global__ __launch_bounds__(kBlock) void embed_forward_kernel(Rows table, int64
 // and rows of dW written once; everything else is small.  A row of dW belongs
 // to one wavefront (one column tile of 512 at a time), which adds its tokens'
 // rows in the order of the text: no atomics on sums, so no order of arrival.
-// Measured, calls behind one another: 301 tokens added to 50257x1600 bf16 8.3 us
+// Measured, calls behind one another: 301 tokens added to 50257x1600 bf16 7.9 us
 // (one launch), 8192 tokens and every row written 81 us (2.3 TB/s of rows),
-// 32769 tokens of 5120 fp16 added to an fp32 half table 148 us (3.4 TB/s).
+// 32769 tokens of 5120 fp16 added to an fp32 half table 143 us (3.5 TB/s).
 
 constexpr int kTileCols = 512;  // 64 lanes of one unit
 constexpr int kFillRows = 64;   // rows of dW that one workgroup looks over for rows without tokens
@@ -90,9 +92,14 @@ __device__ __forceinline__ void fill_rows(const Rows& dw, int64_t row0, uint64_t
   }
 }
 
-// Up to kFew tokens: no sort, one launch where the sorted form has five or six
-// (the border lies where every workgroup's look over all tokens is still a few
-// loads a thread; other borders were not measured).  A workgroup belongs to one token and column
+// Up to kFew tokens: no sort, one launch where the sorted form has four to seven
+// (its counts, a pass for every 9 bits of the row, the sums, the join).  Both
+// forms measured at the same sizes, this one before the sorted one: 512 tokens
+// added to 50257x1600 bf16 7.4 and 37.8 us, with every row written 35.3 and 58.0;
+// 512 onto 32000x4096 8.2 and 38.4; 512 onto 1000x256 7.4 and 33.2; at 65 tokens
+// 7.5 and 35.5.  The border lies on the safe side of where they meet: at 1024
+// tokens this form takes 9.6 and 17.3 us (1600 and 4096 columns) against 39.1 and
+// 44.2, growing with tokens times columns.  A workgroup belongs to one token and column
 // tile; unless an earlier token has the same row it finds the others by
 // comparing, its four wavefronts add a quarter of them each, and the quarters
 // are joined in order.  Workgroups from `sums` on fill the rows without tokens.

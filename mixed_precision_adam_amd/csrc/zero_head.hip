@@ -20,9 +20,10 @@
 // digit of a score (1e-6 at a score of 20).
 //
 // Measured (calls behind one another): 4096 tokens x 50257 words x 1600 columns
-// bf16 2.58 ms, 4096 x 32000 x 4096 fp16 3.04 ms, of which the three products
-// take 91 and 96%, at 700 to 955 and 1000 to 1240 TFLOP/s; losses alone of 33
-// tokens over 50257 x 1600 55 us, of which reading the table takes 34 at least.
+// bf16 2.59 ms, 4096 x 32000 x 4096 fp16 3.06 to 3.17 ms; in a trace, where a
+// pass takes 2.74 and 3.34, the three products are 87 and 91% of it, at 690 to 945
+// and 950 to 1200 TFLOP/s.  Losses alone of 33 tokens over 50257 x 1600 take 56.6
+// us; reading the table at a large copy's rate would take 34.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -523,13 +524,20 @@ __global__ __launch_bounds__(kOneGroup) void mean_kernel(const float* __restrict
 // ------------------------------------------------------------------ sizes
 
 constexpr int64_t kMostVocab = int64_t(1) << 22, kMostCols = int64_t(1) << 16;  // 32-bit offsets within a tile's rows
-// The codes of a block of tokens: as many as fit the 256 MB last-level cache
-// (larger blocks were not measured against it).
+// The codes of a block of tokens: as many as fit the 256 MB last-level cache.
+// Measured with 2^27, 2^28, 2^29 and 2^30 (bf16, workspaces without the table's
+// copy): 4096 tokens x 50257 x 1600 2.96, 2.62, 2.41 and 2.41 ms in 0.78, 1.10,
+// 1.10 and 1.10 GiB, 16384 tokens 11.1, 10.5, 10.1 and 10.4 in 0.78, 1.10, 1.62
+// and 2.72; 4096 x 32000 x 4096 3.32, 3.06, 3.06 and 3.08, 8192 tokens 6.61, 6.22,
+// 6.11 and 6.10.  Half costs 6 to 13%; twice gains 2 to 8% where it spares a block,
+// whose sums of the table's gradient go through memory, for half as much memory
+// again once there are tokens to fill it.
 constexpr int64_t kCodeBytes = int64_t(1) << 28;
 // What a block holds for each element of its hidden rows: copies on 16-byte
 // lines and turned, 2 bytes each, and 4 of the sums before they are rounded.
 // Over a small vocabulary these are what grows with a block, not the codes:
-// 1 GiB for them, 26,112 tokens at 5120 columns.
+// 1 GiB for them, 26,112 tokens at 5120 columns.  Measured with 2^29, 2^30 and
+// 2^31 over 500 words of 4096 columns: 65,536 tokens 3.32, 3.13 and 3.14 ms.
 constexpr int64_t kRowBytes = int64_t(1) << 30;
 constexpr int64_t kCus = 256, kMostParts = 512;
 

@@ -29,8 +29,8 @@ using namespace zero_detail;
 // takes the mean first and then the squares of the differences, which loses
 // nothing where the mean is large.  Both passes move each row once.  Measured,
 // calls behind one another: forward 16384x1600 bf16 34 us (3.1 TB/s), 8 rows
-// 9 us (host time); backward 16384x1600 bf16 78 us (2.0 TB/s), 8191x5120 fp16
-// without the mean 75 us (3.4 TB/s).
+// 8.5 us (host time); backward 16384x1600 bf16 78 us (2.0 TB/s), 8191x5120 fp16
+// without the mean 72.6 us (3.5 TB/s).
 
 constexpr int kWaves = kBlock / 64;
 constexpr int64_t kMaxGroups = int64_t(1) << 20;  // workgroups of one launch; they stride over what is left
@@ -277,8 +277,11 @@ __global__ __launch_bounds__(kJoinWaves * 64) void layernorm_join_kernel(const f
 
 // Workgroups of the backward pass: enough to fill the chip twice over, few
 // enough that their partial rows stay a small part of what is read (512 pairs of
-// fp32 rows against 16384 rows of 16 bits: 4% written and 4% read; other numbers
-// were not measured).
+// fp32 rows against 16384 rows of 16 bits: 4% written and 4% read).  Measured
+// with 256, 512, 1024 and 2048: 16384x1600 bf16 109, 78, 50 and 49 us; 8191x5120
+// fp16 without the mean 93, 72, 82 and 91; 16384x768 42, 34, 43 and 62; 2048x1600
+// 17.3, 14.2, 15.3 and 20.8.  512 is the best of them but for many rows of 1025
+// to 2048 columns, one unit a lane, where twice as many hide more of a row's waits.
 constexpr int64_t kGradGroups = 512;
 constexpr int64_t kLongRow = 1024;  // past it a workgroup shares a row
 

@@ -504,7 +504,8 @@ class ListDecision:
 class _Operator:
     """An operator over tensors of one GPU: its calls run on the current stream of that GPU unless a stream is given.
     It keeps its tensors and its workspace alive: keep it until its calls are done, and give calls that may overlap in
-    time (two streams, two captured graphs) operators of their own."""
+    time (two streams, two captured graphs) operators of their own.  Autograd does not see the calls: tensors that
+    require gradients are taken like others, and results carry no history."""
 
     ws, ws_bytes = None, 0
 
