@@ -294,3 +294,33 @@ def test_hidden_rows_may_be_overwritten_by_their_gradient(tokens, vocab, cols):
     x, dw = h.x.clone(), torch.zeros_like(h.dw)
     op.grad(x, h.labels, h.losses, h.loss, h.count, x, dw)
     assert torch.equal(x, h.dx) and torch.equal(dw, h.dw)
+
+
+@pytest.mark.parametrize("label,others,want", [
+    (math.inf, 0.0, math.nan), (math.nan, 0.0, math.nan), (0.0, math.inf, math.nan), (0.0, math.nan, math.nan),
+    (-math.inf, 0.0, math.inf), (0.0, -math.inf, 0.0), (-math.inf, -math.inf, math.nan),
+    (-math.inf, math.inf, math.nan), (math.inf, -math.inf, math.nan), (1e30, 0.0, 0.0), (0.0, 1e30, 1e30)])
+@pytest.mark.parametrize("vocab", [2, 64, 65, 300])
+def test_losses_of_scores_at_the_ends_of_the_range(label, others, want, vocab):
+    """One score for the label, one for all other words.  1e30 in bf16 is off by half a step of its own."""
+    table = torch.zeros(vocab, 64, dtype=torch.bfloat16, device=DEV)
+    table[:, 0], table[1, 0] = others, label
+    x = torch.zeros(3, 64, dtype=torch.bfloat16, device=DEV)
+    x[:, 0] = 1.0
+    labels = torch.tensor([1, -1, 1], device=DEV)
+    losses, loss = torch.full((3,), 9.0, device=DEV), torch.zeros(1, device=DEV)
+    count = torch.zeros(1, dtype=torch.int64, device=DEV)
+    dx, dw = torch.zeros_like(x), torch.zeros_like(table)
+    op = LossHead(table, max_tokens=3)
+    for call in (lambda: op.forward(x, labels, losses, loss, count),
+                 lambda: op.grad(x, labels, losses, loss, count, dx, dw)):
+        call()
+        assert losses[1].item() == 0.0 and count.item() == 2
+        for got in (losses[0].item(), losses[2].item(), loss.item()):
+            assert got == pytest.approx(want, rel=2.0**-8, nan_ok=True), got
+    assert not dx[1].any()
+    if math.isnan(want):  # the token's factors, so its gradient and every word's
+        assert dx[0, 0].isnan() and dw[:, 0].isnan().all()
+    elif math.isfinite(label) and math.isfinite(others):
+        sure = label > others
+        assert torch.equal(dw[:, 0], torch.zeros_like(dw[:, 0])) if sure else dw[1, 0].item() == -1.0
